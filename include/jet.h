@@ -402,6 +402,136 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
                               void* y, void* workspace, size_t ws_bytes, int B, int T, int D, int H,
                               int dk, int dv, int hidden, int width, jet_dtype dt, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention over a paged key/value cache
+ *
+ * The hybrid model keeps a few softmax-attention layers between its JetBlock
+ * layers, some of them with a sliding window (Jet-Nemotron paper, section
+ * 3.1 and appendix A.1). These calls serve such a layer: the new tokens'
+ * queries and keys are normalised and rotated and their keys and values
+ * enter the cache (jet_attn_rope_append), then the queries attend over it
+ * (jet_attn_paged). A chunk of a prompt, one decode token, or a batch of both
+ * take the same two calls.
+ *
+ * The cache: two pools of pages, [n_pages][Hk][page_size][d] with free
+ *   strides (page_stride, head_stride, row_stride in elements, the same for
+ *   both pools, each a multiple of 16 bytes and at least d elements; element
+ *   stride 1), so pages may also be token-major or hold K and V side by side.
+ *   page_size is a power of two, 16 to 256. Position p of sequence s is row
+ *   p % page_size of page page_table[s][p / page_size].
+ * The batch (all three arrays int32 in DEVICE memory, so a captured graph can
+ *   be replayed with other lengths):
+ *   cu_q [nseq + 1]: the new tokens of sequence s are rows cu_q[s] ..
+ *     cu_q[s+1]-1 of the packed tensors (a sequence may have none; rows from
+ *     cu_q[nseq] up to N are padding and are neither read nor written);
+ *   kv_lens [nseq]: positions of s, the new tokens included: new token i of
+ *     n is at position kv_lens[s] - n + i;
+ *   page_table [nseq][max_pages]: pages of s; entries that no call reaches
+ *     (behind kv_lens, or before every window) are not read.
+ *   Offsets or lengths out of range (cu_q decreasing or above N, kv_lens
+ *   negative or above max_pages * page_size) skip that sequence, and a page
+ *   index outside [0, n_pages) reads as zeros and is not written; both set
+ *   the device error word (JET_ERR_DEVICE from jet_device_error).
+ * Shapes: Hq a multiple of Hk (head h of q reads head h / (Hq / Hk) of the
+ *   cache), Hq <= 256, Hq / Hk <= 64; d a multiple of 16, at most 128;
+ *   nseq <= 65535; max_pages * page_size and N at most 2^30.
+ * q, k, v and the pools have the storage type dt (JET_BF16 or JET_F32); all
+ * arithmetic is float32, results are rounded once.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Per-head RMSNorm of queries and keys, rotation by position, and the append
+ * of keys and values to the cache, in one pass over the new tokens:
+ *   y = x / sqrt(mean_d(x^2) + eps) * gamma; then each pair (y_i, y_{i+rot/2})
+ *   (interleaved: (y_2i, y_2i+1)), i < rot/2, is turned by the angle
+ *   position * inv_freq[i] (formed in float64); elements from rot on are not.
+ *   q [N,Hq,d], k, v [N,Hk,d]: dense rows of heads, q_stride / k_stride /
+ *     v_stride elements between tokens (slices of one projection's output).
+ *   q_gamma, k_gamma [d] float32, or both NULL for no norm.
+ *   inv_freq [rot/2] float32 (may be NULL for rot 0); rot a multiple of 8, at most d.
+ *   q_out [N,Hq,d] with q_out_stride: the rotated queries; may be q itself
+ *     (same stride), otherwise must not overlap an input.
+ *   k and v of every new token go to its position in k_pool / v_pool.
+ * A token without a position (kv_lens[s] below the number of new tokens)
+ * leaves q_out and the cache untouched. Two new tokens never share a
+ * position; sequences that share a page must not both write to it.
+ */
+jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride,
+                                const float* q_gamma, const float* k_gamma, float eps,
+                                const float* inv_freq, int rot, int interleaved,
+                                void* q_out, int64_t q_out_stride,
+                                void* k_pool, void* v_pool,
+                                int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                                const int* cu_q, const int* kv_lens, const int* page_table,
+                                int nseq, int N, int max_pages, int n_pages, int page_size,
+                                int Hq, int Hk, int d, jet_dtype dt, void* stream);
+
+/*
+ * Causal attention of the new tokens over their sequences' cached positions
+ * (the new ones included: append them first):
+ *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j,
+ *   j from max(0, p - window + 1) (0 when window is 0) to p, p the position of token i.
+ *   q [N,Hq,d], q_stride elements between tokens; o [N,Hq,d] dense, must not
+ *     overlap q or the pools. A token that sees no position (p < 0) gets zeros.
+ *   max_new: the largest number of new tokens of a sequence, or 0 if unknown.
+ *     It only chooses the kernel; any value gives correct results.
+ *   workspace: jet_attn_paged_workspace_size bytes (16-byte aligned; independent
+ *     of the cache's lengths), else JET_ERR_WORKSPACE before any launch.
+ *     Contents on entry are ignored; calls that share one must be ordered.
+ */
+size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt);
+jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                          int64_t page_stride, int64_t head_stride, int64_t row_stride,
+                          const int* cu_q, const int* kv_lens, const int* page_table,
+                          void* o, void* workspace, size_t ws_bytes,
+                          int nseq, int N, int max_new, int max_pages, int n_pages, int page_size,
+                          int Hq, int Hk, int d, int window, float scale, jet_dtype dt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Entries of cache pools: copies, forks and compaction
+ *
+ * A pool is any array of equally sized entries in device memory: the pages
+ * of a key/value cache, or the states and histories that
+ * jet_jetblock_decode_slots works on. One call acts on up to 64 pools that
+ * share their entry numbering (K and V of every layer, or states and
+ * histories). pools, entry_bytes (bytes of an entry) and entry_strides
+ * (bytes between entries) are HOST arrays of n_pools; addresses, sizes and
+ * strides are multiples of 16.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * In every pool, entry dst[i] becomes a copy of entry src[i], i < n. src and
+ * dst are HOST arrays, read during the call only. Indices lie in
+ * [0, n_entries), no destination appears twice and no entry is both a source
+ * and a destination (JET_ERR_INVALID_ARG); a source may appear many times
+ * (forks). n = 0 does nothing. One launch for up to 3584 pairs.
+ */
+jet_status jet_cache_copy(void* const* pools, const int64_t* entry_bytes, const int64_t* entry_strides, int n_pools,
+                          int n_entries, const int* src, const int* dst, int n, void* stream);
+
+/*
+ * Moves the live pages of a paged cache to its lowest entries. Live are the
+ * pages that the first ceil(kv_lens[s] / page_size) entries of some sequence's
+ * table name (-1 entries, pages already given up, are skipped; a page that
+ * several tables share is moved once). With n live pages, the live pages at
+ * or above n move, in increasing order, onto the free ones below n, in
+ * increasing order; the pages from n on are free afterwards.
+ *   page_table [nseq][max_pages] and kv_lens [nseq] int32 device memory, as above;
+ *   page_table_out: the rewritten tables (entries behind a sequence's length
+ *     become -1); may be page_table itself, otherwise must not overlap it;
+ *   n_live [1] int32 device memory out: n;
+ *   workspace: jet_cache_compact_workspace_size bytes (16-byte aligned).
+ * n_pages at most 2^20; page_size a power of two. A page index that is
+ * neither -1 nor in range becomes -1, a kv_lens out of range is clamped; both
+ * set the device error word. Two launches, no host read: capturable.
+ */
+size_t jet_cache_compact_workspace_size(int n_pages);
+jet_status jet_cache_compact(void* const* pools, const int64_t* entry_bytes, const int64_t* entry_strides,
+                             int n_pools, int n_pages, int page_size,
+                             const int* page_table, const int* kv_lens, int nseq, int max_pages,
+                             int* page_table_out, int* n_live, void* workspace, size_t ws_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then returns and clears the current device's error
  * word: JET_ERR_TIMEOUT if a bounded in-kernel wait ran out since the last

@@ -12,6 +12,8 @@ Function names match the C entry points:
   jet_jetblock_prefill, jet_jetblock_decode_slots, jet_jetblock_prefill_varlen_workspace_size,
   jet_jetblock_prefill_varlen, jet_jetblock_prefill_range_workspace_size,
   jet_jetblock_prefill_range, jet_gdn_range_compose, jet_gdn_range_correct,
+  jet_attn_rope_append, jet_attn_paged_workspace_size, jet_attn_paged, jet_cache_copy,
+  jet_cache_compact_workspace_size, jet_cache_compact,
   jet_device_error, jet_status_string, jet_launch_count.
 """
 from __future__ import annotations
@@ -34,7 +36,9 @@ EXPORTS = ("jet_kernel_gen", "jet_dyn_conv_v", "jet_gdn_prefill_workspace_size",
            "jet_jetblock_prefill_workspace_size", "jet_jetblock_prefill", "jet_jetblock_decode_slots",
            "jet_jetblock_prefill_varlen_workspace_size", "jet_jetblock_prefill_varlen",
            "jet_jetblock_prefill_range_workspace_size", "jet_jetblock_prefill_range", "jet_gdn_range_compose",
-           "jet_gdn_range_correct", "jet_jetblock_layer_workspace_size", "jet_jetblock_layer", "jet_device_error",
+           "jet_gdn_range_correct", "jet_jetblock_layer_workspace_size", "jet_jetblock_layer",
+           "jet_attn_rope_append", "jet_attn_paged_workspace_size", "jet_attn_paged", "jet_cache_copy",
+           "jet_cache_compact_workspace_size", "jet_cache_compact", "jet_device_error",
            "jet_status_string", "jet_launch_count")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -88,6 +92,15 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.jet_jetblock_layer_workspace_size.argtypes = [I] * 6
     L.jet_jetblock_layer_workspace_size.restype = Z
     L.jet_jetblock_layer.argtypes = [P] * 17 + [Z] + [I] * 9 + [P]
+    Q, F = ctypes.c_int64, ctypes.c_float
+    L.jet_attn_rope_append.argtypes = [P, Q] * 3 + [P, P, F, P, I, I, P, Q, P, P, Q, Q, Q, P, P, P] + [I] * 9 + [P]
+    L.jet_attn_paged_workspace_size.argtypes = [I] * 6
+    L.jet_attn_paged_workspace_size.restype = Z
+    L.jet_attn_paged.argtypes = [P, Q, P, P, Q, Q, Q, P, P, P, P, P, Z] + [I] * 10 + [F, I, P]
+    L.jet_cache_copy.argtypes = [P, P, P, I, I, P, P, I, P]
+    L.jet_cache_compact_workspace_size.argtypes = [I]
+    L.jet_cache_compact_workspace_size.restype = Z
+    L.jet_cache_compact.argtypes = [P, P, P, I, I, I, P, P, I, I, P, P, P, Z, P]
     L.jet_device_error.argtypes = [P]
     L.jet_status_string.argtypes = [I]
     L.jet_status_string.restype = ctypes.c_char_p
@@ -97,7 +110,8 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
               "jet_gdn_decode_step", "jet_jetblock_decode_step", "jet_conv_gdn_decode_step", "jet_jetblock_prefill",
               "jet_jetblock_decode_slots", "jet_jetblock_prefill_varlen", "jet_jetblock_prefill_range",
               "jet_gdn_range_compose",
-              "jet_gdn_range_correct", "jet_jetblock_layer", "jet_device_error"):
+              "jet_gdn_range_correct", "jet_jetblock_layer", "jet_attn_rope_append", "jet_attn_paged", "jet_cache_copy",
+              "jet_cache_compact", "jet_device_error"):
         getattr(L, f).restype = I
     return L
 
@@ -487,6 +501,250 @@ def jet_conv_gdn_decode_step(q, k, v, hist_in, hist_out, taps, g, beta, S, o=Non
         _ptr(o, "o", q.dtype, (B, H, dv)), B, H, dk, dv, dt, _stream(stream))
     _check("jet_conv_gdn_decode_step", st)
     return o
+
+
+# ---------------------------------------------------------------- softmax attention over a paged cache
+class _on:
+    """Make `device` current and issue on `stream` (default: the device's
+    current stream) for the length of a call; what the call allocates belongs
+    to that stream. Every tensor of the call has to be on `device`."""
+
+    def __init__(self, device, stream):
+        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self._stream, self._ctx = stream, None
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        raw = self._stream.cuda_stream if hasattr(self._stream, "cuda_stream") else int(self._stream)
+        if raw:
+            self._ctx = torch.cuda.stream(torch.cuda.ExternalStream(raw))
+            self._ctx.__enter__()
+        return ctypes.c_void_p(raw)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+        return False
+
+
+def _ptr_on(t, name, device, dtype=None, shape=None):
+    if t is None:
+        return None
+    p = _ptr(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return p
+
+
+def _rows(t, name, dtype, shape, device):
+    """[N, heads, d] with dense rows of heads: (address, elements between tokens)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    N, H, d = shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must have dense heads (strides {t.stride()})")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if N > 1 else H * d)
+
+
+def _kv_pools(k_pool, v_pool, dtype, Hk, d, device):
+    """The pools' addresses and their common strides (page, head, row)."""
+    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != 4 or t.shape[1] != Hk or t.shape[3] != d or t.shape != k_pool.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, {Hk}, page, {d}]")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.stride(3) != 1 or t.stride() != k_pool.stride():
+            raise ValueError("k_pool and v_pool must have the same strides and dense rows")
+    st = [k_pool.stride(i) if k_pool.shape[i] > 1 else d for i in range(3)]
+    return ctypes.c_void_p(k_pool.data_ptr()), ctypes.c_void_p(v_pool.data_ptr()), st
+
+
+def _batch(cu_q, kv_lens, page_table, device):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [nseq, max_pages]")
+    nseq, max_pages = page_table.shape
+    return (_ptr_on(cu_q, "cu_q", device, torch.int32, (nseq + 1,)),
+            _ptr_on(kv_lens, "kv_lens", device, torch.int32, (nseq,)),
+            _ptr_on(page_table, "page_table", device, torch.int32), nseq, max_pages)
+
+
+def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, page_table, k_pool, v_pool, q_out=None, *,
+                         eps=1e-6, interleaved=False, stream=None):
+    """Per-head RMSNorm of q [N,Hq,d] and k [N,Hk,d] (gammas [d] float32, or
+    both None: no norm), rotation of their first 2 * len(inv_freq) elements by
+    position * inv_freq (None: no rotation), and the append of k and
+    v [N,Hk,d] to the pools [pages,Hk,page,d]. q, k, v may be slices of one
+    projection's output. cu_q [nseq+1], kv_lens [nseq] (new tokens included)
+    and page_table [nseq,max_pages] are int32 on the GPU. q_out may be q
+    itself. Returns q_out [N,Hq,d]."""
+    L = load_library()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    N, Hq, d = q.shape
+    Hk, dev, dt = k.shape[1], q.device, q.dtype
+    code = _dt(q)
+    qp, qs = _rows(q, "q", dt, (N, Hq, d), dev)
+    kp, ks = _rows(k, "k", dt, (N, Hk, d), dev)
+    vp, vs = _rows(v, "v", dt, (N, Hk, d), dev)
+    kpool, vpool, pst = _kv_pools(k_pool, v_pool, dt, Hk, d, dev)
+    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    gq = _ptr_on(q_gamma, "q_gamma", dev, torch.float32, (d,))
+    gk = _ptr_on(k_gamma, "k_gamma", dev, torch.float32, (d,))
+    fr = _ptr_on(inv_freq, "inv_freq", dev, torch.float32)
+    with _on(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((N, Hq, d), device=dev, dtype=dt)
+        op, os_ = _rows(q_out, "q_out", dt, (N, Hq, d), dev)
+        st = L.jet_attn_rope_append(qp, qs, kp, ks, vp, vs, gq, gk, float(eps), fr, rot, int(bool(interleaved)), op,
+                                    os_, kpool, vpool, *pst, cu, kl, pt, nseq, N, max_pages, k_pool.shape[0],
+                                    k_pool.shape[2], Hq, Hk, d, code, s)
+    _check("jet_attn_rope_append", st)
+    return q_out
+
+
+def jet_attn_paged_workspace_size(nseq: int, N: int, Hq: int, Hk: int, d: int, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of jet_attn_paged for a batch of nseq sequences and N new tokens."""
+    return int(load_library().jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d,
+                                                            JET_BF16 if dtype == torch.bfloat16 else JET_F32))
+
+
+def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 0, o=None, workspace=None, *,
+                   window: int = 0, scale: float | None = None, stream=None):
+    """Causal attention of the new tokens q [N,Hq,d] over the cached positions
+    of their sequences (append theirs first): pools [pages,Hk,page,d], cu_q,
+    kv_lens and page_table as in jet_attn_rope_append. window: positions a
+    token sees, its own included (0: all). scale: 1/sqrt(d) by default.
+    max_new: the largest number of new tokens of a sequence (0: unknown); it
+    only chooses the kernel. Returns o [N,Hq,d]."""
+    L = load_library()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    N, Hq, d = q.shape
+    dev, dt = q.device, q.dtype
+    code = _dt(q)
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("k_pool must be [pages, Hk, page, d]")
+    Hk = k_pool.shape[1]
+    qp, qs = _rows(q, "q", dt, (N, Hq, d), dev)
+    kpool, vpool, pst = _kv_pools(k_pool, v_pool, dt, Hk, d, dev)
+    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, dev)
+    with _on(dev, stream) as s:
+        if o is None:
+            o = torch.empty((N, Hq, d), device=dev, dtype=dt)
+        if workspace is None:
+            workspace = torch.empty(max(16, L.jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, code)), device=dev,
+                                    dtype=torch.uint8)
+        st = L.jet_attn_paged(qp, qs, kpool, vpool, *pst, cu, kl, pt, _ptr_on(o, "o", dev, dt, (N, Hq, d)),
+                              _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size(), nseq,
+                              N, int(max_new), max_pages, k_pool.shape[0], k_pool.shape[2], Hq, Hk, d, int(window),
+                              float(d ** -0.5 if scale is None else scale), code, s)
+    _check("jet_attn_paged", st)
+    return o
+
+
+# ---------------------------------------------------------------- cache entries
+def _entries(pools, what="pools"):
+    """Host arrays (addresses, entry bytes, entry strides) of pools with the
+    same number of entries along their first axis, each entry dense."""
+    if isinstance(pools, torch.Tensor) or len(pools) == 0:
+        raise TypeError(f"{what} must be a non-empty list of tensors")
+    first = pools[0]
+    n = len(pools)
+    base, size, step = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int64 * n)()
+    for i, t in enumerate(pools):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what}[{i}] must be a CUDA tensor")
+        if t.device != first.device:
+            raise ValueError(f"{what}[{i}] is on {t.device}, expected {first.device}")
+        if t.dim() < 2 or t.shape[0] != first.shape[0]:
+            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, expected {first.shape[0]} entries")
+        es = t.element_size()
+        if t.is_contiguous():
+            per = t.numel() // max(1, t.shape[0])
+            dense = True
+        else:      # an entry's dimensions in any order, without gaps
+            per, dense = 1, True
+            for st, sz in sorted((t.stride(j), t.shape[j]) for j in range(1, t.dim()) if t.shape[j] > 1):
+                dense &= st == per
+                per *= sz
+        if not dense:
+            raise ValueError(f"the entries of {what}[{i}] must be dense (strides {t.stride()})")
+        base[i], size[i] = t.data_ptr(), per * es
+        step[i] = t.stride(0) * es if t.shape[0] > 1 else per * es
+    return base, size, step, n, first.shape[0], first.device
+
+
+def _indices(x, name):
+    """Entry numbers as a host int32 array (a list, tuple or CPU tensor)."""
+    if isinstance(x, torch.Tensor):
+        if x.is_cuda:
+            raise TypeError(f"{name} must be on the host: it is checked before the launch")
+        x = x.tolist()
+    return (ctypes.c_int * len(x))(*x)
+
+
+def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
+    """In every pool (tensors [entries, ...] with the same number of entries,
+    each entry dense), entry dst[i] becomes a copy of entry src[i]. src and dst
+    are host lists; a destination appears once and is no source."""
+    L = load_library()
+    base, size, step, n_pools, n_entries, dev = _entries(pools)
+    a, b = _indices(src, "src"), _indices(dst, "dst")
+    if len(a) != len(b):
+        raise ValueError(f"{len(a)} sources for {len(b)} destinations")
+    with _on(dev, stream) as s:
+        st = L.jet_cache_copy(base, size, step, n_pools, n_entries, a, b, len(a), s)
+    _check("jet_cache_copy", st)
+
+
+def jet_cache_compact_workspace_size(n_pages: int) -> int:
+    """Workspace bytes of jet_cache_compact."""
+    return int(load_library().jet_cache_compact_workspace_size(n_pages))
+
+
+def jet_cache_compact(pools, page_table, kv_lens, page_size: int, page_table_out=None, n_live=None, workspace=None, *,
+                      stream=None):
+    """Move the live pages (those that page_table [nseq,max_pages] names within
+    kv_lens [nseq]) of the pools [pages, ...] to the lowest entries. Returns
+    (page_table_out, n_live [1]): the rewritten tables (page_table itself may
+    be given) and the number of live pages, on the GPU."""
+    L = load_library()
+    base, size, step, n_pools, n_pages, dev = _entries(pools)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [nseq, max_pages]")
+    nseq, max_pages = page_table.shape
+    pt = _ptr_on(page_table, "page_table", dev, torch.int32)
+    kl = _ptr_on(kv_lens, "kv_lens", dev, torch.int32, (nseq,))
+    with _on(dev, stream) as s:
+        if page_table_out is None:
+            page_table_out = torch.empty_like(page_table)
+        if n_live is None:
+            n_live = torch.empty(1, device=dev, dtype=torch.int32)
+        if workspace is None:
+            workspace = torch.empty(max(16, L.jet_cache_compact_workspace_size(n_pages)), device=dev,
+                                    dtype=torch.uint8)
+        st = L.jet_cache_compact(base, size, step, n_pools, n_pages, page_size, pt, kl, nseq, max_pages,
+                                 _ptr_on(page_table_out, "page_table_out", dev, torch.int32, (nseq, max_pages)),
+                                 _ptr_on(n_live, "n_live", dev, torch.int32, (1,)),
+                                 _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size(), s)
+    _check("jet_cache_compact", st)
+    return page_table_out, n_live
 
 
 def jet_device_error(stream=None) -> int:

@@ -1,0 +1,301 @@
+// Entry points of the softmax-attention operators and the cache operators:
+// argument checks, kernel selection and launches. Included by jet_api.cu,
+// whose checks and launch helpers it uses.
+#pragma once
+
+namespace {
+
+// what jet_attn_rope_append and jet_attn_paged have in common
+struct AttnShape {
+    int nseq, N, max_pages, n_pages, page_size, Hq, Hk, d;
+    jet_dtype dt;
+};
+
+jet_status check_attn_shape(const AttnShape& a) {
+    if (!dtype_ok(a.dt)) return JET_ERR_INVALID_ARG;
+    if (a.nseq <= 0 || a.N <= 0 || a.max_pages <= 0 || a.n_pages <= 0 || a.page_size <= 0 || a.Hq <= 0 || a.Hk <= 0 ||
+        a.d <= 0 || a.Hq % a.Hk != 0)
+        return JET_ERR_INVALID_ARG;
+    if (elems({a.N, a.Hq, a.d}) < 0 || elems({a.n_pages, a.page_size, a.Hk, a.d}) < 0) return JET_ERR_INVALID_ARG;
+    const bool page_ok = a.page_size >= 16 && a.page_size <= 256 && (a.page_size & (a.page_size - 1)) == 0;
+    if (a.d % 16 != 0 || a.d > 128 || !page_ok || a.Hq > 256 || a.Hq / a.Hk > 64 || a.nseq > 65535 ||
+        (long long)a.max_pages * a.page_size > 0x40000000LL || a.N > 0x40000000)
+        return JET_ERR_UNSUPPORTED;
+    return JET_OK;
+}
+
+int page_shift_of(int page_size) {
+    int sh = 0;
+    while ((1 << sh) < page_size) ++sh;
+    return sh;
+}
+
+// strides of the pools, in elements: rows of d elements that start 16-byte
+// aligned and do not overlap their neighbours
+jet_status check_pools(const AttnShape& a, const void* k, const void* v, int64_t page_stride, int64_t head_stride,
+                       int64_t row_stride) {
+    const int64_t align = 16 / (int64_t)esize(a.dt);
+    for (int64_t st : {page_stride, head_stride, row_stride}) {
+        if (st < a.d || st > (1LL << 38)) return JET_ERR_INVALID_ARG;
+        if (st % align != 0) return JET_ERR_MISALIGNED;
+    }
+    if (!aligned16(k) || !aligned16(v)) return JET_ERR_MISALIGNED;
+    return JET_OK;
+}
+
+// bytes from the first to behind the last element of a pool
+size_t pool_extent(const AttnShape& a, int64_t page_stride, int64_t head_stride, int64_t row_stride) {
+    return esize(a.dt) * (size_t)((a.n_pages - 1) * page_stride + (a.Hk - 1) * head_stride +
+                                  (a.page_size - 1) * row_stride + a.d);
+}
+
+template <typename T>
+jet_status launch_append(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
+    // four tokens to a block once that still fills the GPU several times over
+    const bool wide = b.N >= 4 * 4 * kMaxSMs;
+    if (a.d > 64)
+        return wide ? launch(attn::append_kernel<T, 4, 16>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b)
+                    : launch(attn::append_kernel<T, 1, 16>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+    return wide ? launch(attn::append_kernel<T, 4, 8>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b)
+                : launch(attn::append_kernel<T, 1, 8>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+}
+
+template <typename T>
+jet_status launch_attn_simt(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o,
+                            int Hq, int Hk, int d, int window, float scale, cudaStream_t s) {
+    const dim3 grid(b.N, (Hq + attn::SIMT_WARPS - 1) / attn::SIMT_WARPS);
+    return launch(attn::attn_simt_kernel<T>, grid, dim3(attn::SIMT_WARPS * 32), 0, s, (const T*)q,
+                  (long long)q_stride, c, b, (T*)o, Hq, Hk, d, window, scale);
+}
+
+}  // namespace
+
+extern "C" {
+
+jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const float* q_gamma, const float* k_gamma, float eps,
+                                const float* inv_freq, int rot, int interleaved, void* q_out, int64_t q_out_stride,
+                                void* k_pool, void* v_pool, int64_t page_stride, int64_t head_stride,
+                                int64_t row_stride, const int* cu_q, const int* kv_lens, const int* page_table,
+                                int nseq, int N, int max_pages, int n_pages, int page_size, int Hq, int Hk, int d,
+                                jet_dtype dt, void* stream) {
+    if (!q || !k || !v || !q_out || !k_pool || !v_pool || !cu_q || !kv_lens || !page_table) return JET_ERR_INVALID_ARG;
+    if ((q_gamma == nullptr) != (k_gamma == nullptr)) return JET_ERR_INVALID_ARG;
+    const AttnShape a{nseq, N, max_pages, n_pages, page_size, Hq, Hk, d, dt};
+    jet_status st = check_attn_shape(a);
+    if (st != JET_OK) return st;
+    if (rot < 0 || rot > d || (rot > 0 && !inv_freq)) return JET_ERR_INVALID_ARG;
+    if (q_gamma && !(eps >= 0.f && eps < INFINITY)) return JET_ERR_INVALID_ARG;
+    if (rot % 8 != 0) return JET_ERR_UNSUPPORTED;
+    const size_t es = esize(dt);
+    const int64_t kMaxStride = 1LL << 38;
+    for (auto [sd, heads] : {std::pair<int64_t, int>{q_stride, Hq}, {k_stride, Hk}, {v_stride, Hk},
+                             {q_out_stride, Hq}}) {
+        if (sd < (int64_t)heads * d || sd > kMaxStride) return JET_ERR_INVALID_ARG;
+        if (sd % 8 != 0) return JET_ERR_MISALIGNED;
+    }
+    st = check_pools(a, k_pool, v_pool, page_stride, head_stride, row_stride);
+    if (st != JET_OK) return st;
+    for (const void* p : {q, k, v, (const void*)q_out})
+        if (!aligned16(p)) return JET_ERR_MISALIGNED;
+    for (const void* p : {(const void*)q_gamma, (const void*)k_gamma, (const void*)inv_freq, (const void*)cu_q,
+                          (const void*)kv_lens, (const void*)page_table})
+        if (!aligned_to(p, 4)) return JET_ERR_MISALIGNED;
+    auto span = [&](int64_t sd, int heads) { return es * (size_t)((int64_t)(N - 1) * sd + (int64_t)heads * d); };
+    // in place over q (same rows), or apart from every input; the pools apart from all of them
+    if (!(q_out == q && q_out_stride == q_stride))
+        for (auto [p, n] : {std::pair<const void*, size_t>{q, span(q_stride, Hq)}, {k, span(k_stride, Hk)},
+                            {v, span(v_stride, Hk)}})
+            if (overlap(q_out, span(q_out_stride, Hq), p, n)) return JET_ERR_INVALID_ARG;
+    const size_t ext = pool_extent(a, page_stride, head_stride, row_stride);
+    for (const void* pool : {(const void*)k_pool, (const void*)v_pool})
+        for (auto [p, n] : {std::pair<const void*, size_t>{q, span(q_stride, Hq)}, {k, span(k_stride, Hk)},
+                            {v, span(v_stride, Hk)}, {q_out, span(q_out_stride, Hq)}})
+            if (overlap(pool, ext, p, n)) return JET_ERR_INVALID_ARG;
+    if (k_pool == v_pool) return JET_ERR_INVALID_ARG;
+    const attn::AppendArgs args{q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_gamma, k_gamma, inv_freq, q_out,
+                                Hq, Hk, d, rot, interleaved != 0, eps};
+    const attn::Cache c{k_pool, v_pool, page_stride, head_stride, row_stride, page_table, max_pages, n_pages,
+                        page_shift_of(page_size)};
+    const attn::Batch b{cu_q, kv_lens, nseq, N};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dt == JET_BF16 ? launch_append<__nv_bfloat16>(args, c, b, s) : launch_append<float>(args, c, b, s);
+}
+
+size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt) {
+    if (check_attn_shape(AttnShape{nseq, N, 1, 1, 16, Hq, Hk, d, dt}) != JET_OK) return 0;
+    return 16;
+}
+
+jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                          int64_t page_stride, int64_t head_stride, int64_t row_stride, const int* cu_q,
+                          const int* kv_lens, const int* page_table, void* o, void* workspace, size_t ws_bytes,
+                          int nseq, int N, int max_new, int max_pages, int n_pages, int page_size, int Hq, int Hk,
+                          int d, int window, float scale, jet_dtype dt, void* stream) {
+    if (!q || !k_pool || !v_pool || !cu_q || !kv_lens || !page_table || !o) return JET_ERR_INVALID_ARG;
+    const AttnShape a{nseq, N, max_pages, n_pages, page_size, Hq, Hk, d, dt};
+    jet_status st = check_attn_shape(a);
+    if (st != JET_OK) return st;
+    if (window < 0 || max_new < 0 || !(scale > 0.f && scale < INFINITY)) return JET_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)Hq * d || q_stride > (1LL << 38)) return JET_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0) return JET_ERR_MISALIGNED;
+    st = check_pools(a, k_pool, v_pool, page_stride, head_stride, row_stride);
+    if (st != JET_OK) return st;
+    for (const void* p : {q, (const void*)o, (const void*)workspace})
+        if (!aligned16(p)) return JET_ERR_MISALIGNED;
+    for (const int* p : {cu_q, kv_lens, page_table})
+        if (!aligned_to(p, 4)) return JET_ERR_MISALIGNED;
+    const size_t es = esize(dt), on = es * (size_t)N * Hq * d;
+    const size_t qn = es * (size_t)((int64_t)(N - 1) * q_stride + (int64_t)Hq * d);
+    const size_t ext = pool_extent(a, page_stride, head_stride, row_stride);
+    if (overlap(o, on, q, qn) || overlap(o, on, k_pool, ext) || overlap(o, on, v_pool, ext)) return JET_ERR_INVALID_ARG;
+    if (!workspace) ws_bytes = 0;
+    if (ws_bytes < jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, dt)) return JET_ERR_WORKSPACE;
+    const attn::Cache c{k_pool, v_pool, page_stride, head_stride, row_stride, page_table, max_pages, n_pages,
+                        page_shift_of(page_size)};
+    const attn::Batch b{cu_q, kv_lens, nseq, N};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dt == JET_BF16 ? launch_attn_simt<__nv_bfloat16>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s)
+                          : launch_attn_simt<float>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- cache operators
+namespace {
+
+jet_status make_pools(cache::Pools& P, void* const* pools, const int64_t* entry_bytes, const int64_t* entry_strides,
+                      int n_pools, int n_entries) {
+    if (!pools || !entry_bytes || !entry_strides || n_pools <= 0 || n_entries <= 0) return JET_ERR_INVALID_ARG;
+    if (n_pools > cache::MAX_POOLS) return JET_ERR_UNSUPPORTED;
+    P = cache::Pools{};
+    P.n = n_pools;
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i] || entry_bytes[i] <= 0 || entry_strides[i] < entry_bytes[i] || entry_bytes[i] > (1LL << 40) ||
+            entry_strides[i] > (1LL << 40))
+            return JET_ERR_INVALID_ARG;
+        if (!aligned16(pools[i]) || entry_bytes[i] % 16 != 0 || entry_strides[i] % 16 != 0) return JET_ERR_MISALIGNED;
+        P.base[i] = static_cast<unsigned char*>(pools[i]);
+        P.stride[i] = entry_strides[i];
+        P.bytes[i] = entry_bytes[i];
+    }
+    return JET_OK;
+}
+
+// blocks for n entries of every pool: one piece each, at most eight blocks to an SM
+unsigned copy_grid(const cache::Pools& P, long long n) {
+    long long pieces = 0;
+    for (int i = 0; i < P.n; ++i) pieces += (P.bytes[i] + cache::PIECE - 1) / cache::PIECE * n;
+    return (unsigned)std::max<long long>(1, std::min<long long>(pieces, 8 * kMaxSMs));
+}
+
+// Every index in range, every destination once and none also a source. One
+// bit per entry for each of the two sets; on the stack for the usual pools.
+jet_status check_pairs(const int* src, const int* dst, int n, int n_entries) {
+    constexpr int kStackWords = 2048;
+    uint32_t stack[2 * kStackWords];
+    const size_t words = ((size_t)n_entries + 31) / 32;
+    uint32_t* mem = stack;
+    void* heap = nullptr;
+    if (words > kStackWords) {
+        heap = std::calloc(2 * words, sizeof(uint32_t));
+        if (!heap) return JET_ERR_INVALID_ARG;
+        mem = static_cast<uint32_t*>(heap);
+    } else {
+        std::memset(stack, 0, 2 * words * sizeof(uint32_t));
+    }
+    uint32_t *is_src = mem, *is_dst = mem + words;
+    jet_status st = JET_OK;
+    for (int i = 0; i < n && st == JET_OK; ++i) {
+        const int a = src[i], b = dst[i];
+        if (a < 0 || a >= n_entries || b < 0 || b >= n_entries) { st = JET_ERR_INVALID_ARG; break; }
+        if (is_dst[b >> 5] >> (b & 31) & 1u) st = JET_ERR_INVALID_ARG;
+        is_src[a >> 5] |= 1u << (a & 31);
+        is_dst[b >> 5] |= 1u << (b & 31);
+    }
+    for (int i = 0; i < n && st == JET_OK; ++i)
+        if (is_src[dst[i] >> 5] >> (dst[i] & 31) & 1u) st = JET_ERR_INVALID_ARG;
+    std::free(heap);
+    return st;
+}
+
+template <int CAP>
+jet_status launch_copy(const cache::Pools& P, const int* src, const int* dst, int n, cudaStream_t s) {
+    cache::Pairs<CAP> pairs;
+    for (int i = 0; i < n; ++i) pairs.e[i] = make_int2(src[i], dst[i]);
+    return launch(cache::copy_kernel<CAP>, dim3(copy_grid(P, n)), dim3(cache::THREADS), 0, s, P, pairs, n);
+}
+
+constexpr int kFewPairs = 256, kManyPairs = 3584;     // 2 KB and 28 KB of kernel parameters
+constexpr int kMaxCompactPages = 1 << 20;             // the plan's bitmap: 128 KB of shared memory
+
+}  // namespace
+
+extern "C" {
+
+jet_status jet_cache_copy(void* const* pools, const int64_t* entry_bytes, const int64_t* entry_strides, int n_pools,
+                          int n_entries, const int* src, const int* dst, int n, void* stream) {
+    cache::Pools P;
+    jet_status st = make_pools(P, pools, entry_bytes, entry_strides, n_pools, n_entries);
+    if (st != JET_OK) return st;
+    if (n < 0 || (n > 0 && (!src || !dst))) return JET_ERR_INVALID_ARG;
+    if (n == 0) return JET_OK;
+    st = check_pairs(src, dst, n, n_entries);
+    if (st != JET_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    for (int i = 0; i < n && st == JET_OK; i += kManyPairs) {
+        const int m = std::min(n - i, kManyPairs);
+        st = m <= kFewPairs ? launch_copy<kFewPairs>(P, src + i, dst + i, m, s)
+                            : launch_copy<kManyPairs>(P, src + i, dst + i, m, s);
+    }
+    return st;
+}
+
+size_t jet_cache_compact_workspace_size(int n_pages) {
+    if (n_pages <= 0 || n_pages > kMaxCompactPages) return 0;
+    return 256 + sizeof(int2) * (size_t)((n_pages / 2 + 32) & ~31) + sizeof(int) * (size_t)n_pages;
+}
+
+jet_status jet_cache_compact(void* const* pools, const int64_t* entry_bytes, const int64_t* entry_strides,
+                             int n_pools, int n_pages, int page_size, const int* page_table, const int* kv_lens,
+                             int nseq, int max_pages, int* page_table_out, int* n_live, void* workspace,
+                             size_t ws_bytes, void* stream) {
+    cache::Pools P;
+    jet_status st = make_pools(P, pools, entry_bytes, entry_strides, n_pools, n_pages);
+    if (st != JET_OK) return st;
+    if (!page_table || !kv_lens || !page_table_out || !n_live || nseq <= 0 || max_pages <= 0 || page_size <= 0)
+        return JET_ERR_INVALID_ARG;
+    const long long cells = elems({nseq, max_pages});
+    if (cells < 0) return JET_ERR_INVALID_ARG;
+    if (n_pages > kMaxCompactPages || (page_size & (page_size - 1)) != 0 ||
+        (long long)max_pages * page_size > 0x40000000LL)
+        return JET_ERR_UNSUPPORTED;
+    for (const void* p : {(const void*)page_table, (const void*)kv_lens, (const void*)page_table_out,
+                          (const void*)n_live})
+        if (!aligned_to(p, 4)) return JET_ERR_MISALIGNED;
+    if (!aligned16(workspace)) return JET_ERR_MISALIGNED;
+    if (!workspace) ws_bytes = 0;
+    if (ws_bytes < jet_cache_compact_workspace_size(n_pages)) return JET_ERR_WORKSPACE;
+    const size_t tb = sizeof(int) * (size_t)cells;
+    if (page_table_out != page_table && overlap(page_table_out, tb, page_table, tb)) return JET_ERR_INVALID_ARG;
+    if (overlap(n_live, 4, page_table, tb) || overlap(n_live, 4, page_table_out, tb) ||
+        overlap(n_live, 4, kv_lens, sizeof(int) * (size_t)nseq) ||
+        overlap(page_table_out, tb, kv_lens, sizeof(int) * (size_t)nseq))
+        return JET_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const size_t moves_bytes = sizeof(int2) * (size_t)((n_pages / 2 + 32) & ~31);
+    const cache::PlanOut plan{reinterpret_cast<int*>(w), reinterpret_cast<int2*>(w + 256),
+                              reinterpret_cast<int*>(w + 256 + moves_bytes)};
+    const int shift = page_shift_of(page_size);
+    const size_t smem = sizeof(uint32_t) * (((size_t)n_pages + 31) / 32);
+    if (smem_attr(cache::compact_plan_kernel, smem) != JET_OK) return JET_ERR_CUDA;
+    st = launch(cache::compact_plan_kernel, dim3(1), dim3(cache::PLAN_THREADS), smem, s, page_table, kv_lens, nseq,
+                max_pages, shift, n_pages, plan, n_live);
+    if (st != JET_OK) return st;
+    // the number of moves is known on the device only: at most half the pages
+    return launch(cache::compact_move_kernel, dim3(copy_grid(P, std::max(1, n_pages / 2))), dim3(cache::THREADS), 0, s,
+                  P, page_table, page_table_out, kv_lens, nseq, max_pages, shift, n_pages, (const int*)n_live, plan);
+}
+
+}  // extern "C"

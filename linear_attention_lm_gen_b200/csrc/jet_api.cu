@@ -8,13 +8,20 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <tuple>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
+#include "k_attn_append.cuh"
+#include "k_attn_common.cuh"
+#include "k_attn_simt.cuh"
+#include "k_cache.cuh"
 #include "k_decode.cuh"
 #include "k_gen.cuh"
 #include "k_genconv.cuh"
@@ -1304,6 +1311,8 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
     if (!h) return JET_ERR_CUDA;
     return gemm_rm(h, o, wo, y, N, D, H * dv, false);
 }
+
+#include "attn_api.cuh"
 
 #ifdef JET_TEST_WAIT_EXPIRY
 // test builds only: see g_test_skip_p2a
