@@ -434,7 +434,7 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
  *   the device error word (JET_ERR_DEVICE from jet_device_error).
  * Shapes: Hq a multiple of Hk (head h of q reads head h / (Hq / Hk) of the
  *   cache), Hq <= 256, Hq / Hk <= 64; d a multiple of 16, at most 128;
- *   nseq <= 65535; max_pages * page_size and N at most 2^30.
+ *   nseq <= 65535; max_pages * page_size at most 2^30 and N at most 2^24.
  * q, k, v and the pools have the storage type dt (JET_BF16 or JET_F32); all
  * arithmetic is float32, results are rounded once.
  * ---------------------------------------------------------------------- */

@@ -19,7 +19,7 @@ jet_status check_attn_shape(const AttnShape& a) {
     if (elems({a.N, a.Hq, a.d}) < 0 || elems({a.n_pages, a.page_size, a.Hk, a.d}) < 0) return JET_ERR_INVALID_ARG;
     const bool page_ok = a.page_size >= 16 && a.page_size <= 256 && (a.page_size & (a.page_size - 1)) == 0;
     if (a.d % 16 != 0 || a.d > 128 || !page_ok || a.Hq > 256 || a.Hq / a.Hk > 64 || a.nseq > 65535 ||
-        (long long)a.max_pages * a.page_size > 0x40000000LL || a.N > 0x40000000)
+        (long long)a.max_pages * a.page_size > 0x40000000LL || a.N > (1 << 24))
         return JET_ERR_UNSUPPORTED;
     return JET_OK;
 }
@@ -66,6 +66,49 @@ jet_status launch_attn_simt(const void* q, int64_t q_stride, const attn::Cache& 
     const dim3 grid(b.N, (Hq + attn::SIMT_WARPS - 1) / attn::SIMT_WARPS);
     return launch(attn::attn_simt_kernel<T>, grid, dim3(attn::SIMT_WARPS * 32), 0, s, (const T*)q,
                   (long long)q_stride, c, b, (T*)o, Hq, Hk, d, window, scale);
+}
+
+// Workspace of a split attention launch: two slots per CTA.
+struct SlotLayout {
+    size_t ml, bytes;
+};
+SlotLayout slot_layout(int n_cta, int rows, int d) {
+    const size_t o = sizeof(float) * (size_t)n_cta * 2 * rows * d;
+    return SlotLayout{o, o + sizeof(float2) * (size_t)n_cta * 2 * rows};
+}
+attn::Slots make_slots(void* ws, int n_cta, int rows, int d) {
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    return attn::Slots{reinterpret_cast<float*>(p), reinterpret_cast<float2*>(p + slot_layout(n_cta, rows, d).ml), rows};
+}
+
+// tiles of `rows` query rows: whole tokens, or parts of one token's heads
+attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, int window, int rows, int kt, int c0,
+                     int min_chunk) {
+    const int gt = std::min(G, rows);
+    return attn::Work{b, c, Hk, G, window, std::max(1, rows / G), gt, (G + gt - 1) / gt, kt, c0, min_chunk};
+}
+
+jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
+    const int per = attn::JOIN_WARPS * 4;         // at most four rows to a warp
+    const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
+    return launch(attn::attn_join_kernel<__nv_bfloat16>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, w, sl,
+                  (__nv_bfloat16*)o, d, n_cta);
+}
+
+template <int DP>
+jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o,
+                              void* ws, int Hk, int G, int d, int window, float scale, cudaStream_t s) {
+    typedef attn::DecCfg<DP> C;
+    const int n_cta = launch_sms() * C::CTAS;
+    // an item's start and end cost a CTA about as much as 96 positions; parts
+    // below 256 positions are not worth joining
+    const attn::Work w = make_work(c, b, Hk, G, window, attn::DEC_ROWS, attn::DEC_KT, 96, 256);
+    const attn::Slots sl = make_slots(ws, n_cta, attn::DEC_ROWS, d);
+    auto kern = attn::attn_decode_kernel<DP>;
+    if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
+    const jet_status st = launch(kern, dim3(n_cta), dim3(attn::DEC_THREADS), C::SMEM, s, (const __nv_bfloat16*)q,
+                                 (long long)q_stride, w, sl, (__nv_bfloat16*)o, d, scale * 1.44269504f);
+    return st != JET_OK ? st : launch_join(w, sl, o, d, n_cta, s);
 }
 
 }  // namespace
@@ -124,7 +167,9 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
 
 size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt) {
     if (check_attn_shape(AttnShape{nseq, N, 1, 1, 16, Hq, Hk, d, dt}) != JET_OK) return 0;
-    return 16;
+    if (dt != JET_BF16) return 16;
+    const int per_sm = d <= 64 ? attn::DecCfg<64>::CTAS : attn::DecCfg<128>::CTAS;
+    return slot_layout(kMaxSMs * per_sm, attn::DEC_ROWS, d).bytes;
 }
 
 jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
@@ -155,8 +200,9 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
                         page_shift_of(page_size)};
     const attn::Batch b{cu_q, kv_lens, nseq, N};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dt == JET_BF16 ? launch_attn_simt<__nv_bfloat16>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s)
-                          : launch_attn_simt<float>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s);
+    if (dt == JET_F32) return launch_attn_simt<float>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s);
+    return d <= 64 ? launch_attn_decode<64>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
+                   : launch_attn_decode<128>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
 }
 
 }  // extern "C"

@@ -20,6 +20,8 @@
 #include "common.cuh"
 #include "k_attn_append.cuh"
 #include "k_attn_common.cuh"
+#include "k_attn_decode.cuh"
+#include "k_attn_sched.cuh"
 #include "k_attn_simt.cuh"
 #include "k_cache.cuh"
 #include "k_decode.cuh"

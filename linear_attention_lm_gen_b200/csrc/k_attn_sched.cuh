@@ -1,0 +1,252 @@
+// How the attention kernels divide a ragged batch among a fixed grid.
+//
+// An item is a tile of query rows of one sequence and one cache head: `tpt`
+// tokens times `gt` of the G query heads that share the head (`hs` such head
+// parts, one unless G exceeds the tile's rows). Its cost is taken as the
+// positions it reads plus a constant c0. The items lie one after another on
+// an axis, sequence by sequence, head by head, tile by tile, and CTA c works
+// on the interval [c * chunk, (c + 1) * chunk): every CTA gets the same cost
+// whatever the lengths are, a long sequence is split along the cache as a
+// matter of course, and the grid needs no length on the host. An item that
+// lies in one interval is finished by its CTA; the parts of an item that is
+// cut go to the workspace (each CTA has at most one part of an item that
+// began before its interval, slot 0, and one of an item that goes on behind
+// it, slot 1) and a second kernel joins them in order, so results do not
+// depend on timing and the workspace not on the lengths.
+//
+// The cost of tile i of a sequence with A = max(0, L - n) older positions is
+// c0 + A + (i + 1) tpt, or c0 + tpt + window - 1 once the window cuts the
+// first positions off, so that sums over tiles have a closed form.
+#pragma once
+#include "k_attn_common.cuh"
+
+namespace jet {
+namespace attn {
+
+struct Work {
+    Batch b;
+    Cache c;
+    int Hk, G, window;
+    int tpt, gt, hs;      // tokens and heads of a tile, head parts
+    int kt;               // positions of a step along the cache (a power of two)
+    int c0, min_chunk;
+};
+
+__device__ __forceinline__ long long tiles_cost(const Work& w, long long A, long long i) {
+    long long m = i;
+    if (w.window > 0) {
+        const long long first = (w.window - 1 - A + w.tpt - 1) / w.tpt;      // first tile the window cuts
+        m = min(i, max(0LL, first));
+    }
+    return m * (w.c0 + A) + w.tpt * (m * (m + 1) / 2) + (i - m) * ((long long)w.c0 + w.tpt + w.window - 1);
+}
+
+__device__ __forceinline__ int seq_tiles(const Work& w, const Seq& q) { return (q.n + w.tpt - 1) / w.tpt; }
+__device__ __forceinline__ long long seq_cost(const Work& w, const Seq& q) {
+    return tiles_cost(w, max(0, q.L - q.n), seq_tiles(w, q)) * (w.Hk * w.hs);
+}
+
+// one item: its place on the axis and what it covers
+struct Item {
+    int s, hh, i;              // sequence, head * hs + head part, tile
+    Seq q;
+    long long a, cost;         // start and length on the axis
+    int t0, nt;                // first token, tokens
+    int lo, hi;                // positions read (lo a multiple of the step), empty if hi <= 0
+    int steps;
+
+    __device__ __forceinline__ void fill(const Work& w) {
+        const long long A = max(0, q.L - q.n);
+        cost = tiles_cost(w, A, i + 1) - tiles_cost(w, A, i);
+        t0 = i * w.tpt;
+        nt = min(w.tpt, q.n - t0);
+        const int p0 = q.L - q.n + t0;
+        lo = first_key(p0, w.window) & ~(w.kt - 1);
+        hi = p0 + nt;
+        steps = hi > lo ? (hi - lo + w.kt - 1) / w.kt : 0;
+    }
+    // first step at or behind place x of the axis
+    __device__ __forceinline__ int step_at(long long x) const {
+        if (x <= a) return 0;
+        if (x >= a + cost) return steps;
+        return (int)((x - a) * steps / cost);
+    }
+    __device__ __forceinline__ void next(const Work& w) {
+        a += cost;
+        if (++i >= seq_tiles(w, q)) {
+            i = 0;
+            if (++hh >= w.Hk * w.hs) {
+                hh = 0;
+                do {
+                    if (++s >= w.b.nseq) return;
+                    q = load_seq(w.b, w.c, s, false);
+                } while (q.n == 0);
+            }
+        }
+        fill(w);
+    }
+};
+
+// The axis's length and step, and the item at place index * chunk of it.
+// Every thread of the block (THREADS of them) calls it; `item` is the same in
+// all of them. Returns false where the place lies behind the end.
+template <int THREADS>
+__device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index, long long& chunk, long long& total,
+                                             Item& item) {
+    __shared__ long long part[THREADS / 32];
+    __shared__ long long found_a;
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (w.b.nseq + THREADS - 1) / THREADS;
+    const int s0 = min(w.b.nseq, tid * per), s1 = min(w.b.nseq, s0 + per);
+    long long sum = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = load_seq(w.b, w.c, s, true);
+        if (q.n > 0) sum += seq_cost(w, q);
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    long long before = inc - sum;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += part[i];
+        total += part[i];
+    }
+    chunk = max((long long)w.min_chunk, (total + n_cta - 1) / n_cta);
+    const long long x = chunk * index;
+    if (x >= total) return false;
+    if (x >= before && x < before + sum) {
+        for (int s = s0; s < s1; ++s) {
+            const Seq q = load_seq(w.b, w.c, s, false);
+            const long long cost = q.n > 0 ? seq_cost(w, q) : 0;
+            if (x < before + cost) {
+                const long long A = max(0, q.L - q.n), per_head = cost / (w.Hk * w.hs);
+                const long long hh = (x - before) / per_head, rem = (x - before) - hh * per_head;
+                int lo = 0, hi = seq_tiles(w, q) - 1;          // largest tile that starts at or before rem
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (tiles_cost(w, A, mid) <= rem) lo = mid;
+                    else hi = mid - 1;
+                }
+                found[0] = s;
+                found[1] = (int)hh;
+                found[2] = lo;
+                found_a = before + hh * per_head + tiles_cost(w, A, lo);
+                break;
+            }
+            before += cost;
+        }
+    }
+    __syncthreads();
+    item.s = found[0];
+    item.hh = found[1];
+    item.i = found[2];
+    item.a = found_a;
+    item.q = load_seq(w.b, w.c, item.s, false);
+    item.fill(w);
+    return true;
+}
+
+// Workspace: per CTA two slots, each `rows` rows of d float32 sums and the
+// rows' (maximum, sum) pairs, in units of base-2 logits.
+struct Slots {
+    float* o;          // [n_cta * 2][rows][d]
+    float2* ml;        // [n_cta * 2][rows]
+    int rows;
+};
+
+// element offset of row r of an item in the packed [N, Hq, d] outputs, or -1
+__device__ __forceinline__ long long out_row(const Work& w, const Item& it, int r, int d) {
+    const int tok = r / w.gt, g = r - tok * w.gt;
+    const int part = it.hh % w.hs, h = it.hh / w.hs;
+    const int head = part * w.gt + g;
+    if (tok >= it.nt || head >= w.G) return -1;
+    return ((long long)(it.q.r0 + it.t0 + tok) * (w.Hk * w.G) + h * w.G + head) * d;
+}
+
+// Joins the parts of the items that were cut: block x of the grid looks at
+// the place where CTA x + 1 begins and takes the item there if the item's
+// first part is CTA x's. One warp per row.
+constexpr int JOIN_WARPS = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(JOIN_WARPS * 32)
+attn_join_kernel(Work w, Slots sl, T* __restrict__ o, int d, int n_cta) {
+    // cu_q and kv_lens are final before the kernel ahead of this one began
+    long long chunk, total;
+    Item it;
+    const int first = blockIdx.x;
+    const bool inside = block_locate<JOIN_WARPS * 32>(w, n_cta, first + 1, chunk, total, it);
+    pdl_wait();        // in every block: the next kernel's wait covers the parts' kernel through this one
+    pdl_trigger();
+    if (!inside) return;
+    const long long x = chunk * (first + 1);
+    if (it.a == x || it.a < x - chunk) return;              // not cut here, or not here first
+    const int last = (int)((it.a + it.cost - 1) / chunk);
+    const int lane = threadIdx.x & 31;
+    const int rows = min(sl.rows, it.nt * w.gt);
+    for (int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); r < rows; r += gridDim.y * JOIN_WARPS) {
+        const long long dst = out_row(w, it, r, d);
+        if (dst < 0) continue;
+        float M = -INFINITY;
+        int parts = 0;
+        for (int k = first + lane; k <= last; k += 32) {
+            const int b = it.step_at(chunk * k), e = it.step_at(chunk * (k + 1));
+            if (b >= e) continue;
+            ++parts;
+            M = fmaxf(M, sl.ml[(k * 2 + (k == first ? 1 : 0)) * (long long)sl.rows + r].x);
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+            parts += __shfl_xor_sync(0xffffffffu, parts, m);
+        }
+        if (parts <= 1) continue;            // one part holds all steps: its CTA wrote the row
+        const float base = M == -INFINITY ? 0.f : M;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+        for (int k0 = first; k0 <= last; k0 += 32) {
+            const int k = k0 + lane;
+            float wt = 0.f;
+            bool on = false;
+            if (k <= last) {
+                on = it.step_at(chunk * k) < it.step_at(chunk * (k + 1));
+                if (on) {
+                    const float2 ml = sl.ml[(k * 2 + (k == first ? 1 : 0)) * (long long)sl.rows + r];
+                    wt = exp2f(ml.x - base);
+                    l += wt * ml.y;
+                }
+            }
+            const unsigned any = __ballot_sync(0xffffffffu, on);
+            const int cnt = min(32, last - k0 + 1);
+#pragma unroll 4
+            for (int j = 0; j < cnt; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, wt, j);
+                if (!(any >> j & 1u)) continue;
+                const float* src = sl.o + ((k0 + j) * 2 + (k0 + j == first ? 1 : 0)) * (long long)sl.rows * d +
+                                   (long long)r * d + lane * 4;
+                if (lane * 4 < d) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    acc[0] = fmaf(wj, v.x, acc[0]);
+                    acc[1] = fmaf(wj, v.y, acc[1]);
+                    acc[2] = fmaf(wj, v.z, acc[2]);
+                    acc[3] = fmaf(wj, v.w, acc[3]);
+                }
+            }
+        }
+        l = warp_sum(l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (lane * 4 < d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Elem<T>::st(o + dst + lane * 4 + e, acc[e] * inv);
+    }
+}
+
+}  // namespace attn
+}  // namespace jet
