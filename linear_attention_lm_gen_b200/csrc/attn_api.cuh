@@ -111,6 +111,45 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     return st != JET_OK ? st : launch_join(w, sl, o, d, n_cta, s);
 }
 
+// pool [n_pages][Hk][page][d] as a 4-D tensor (d, page, Hk, n_pages): a box is 64 columns of up to 128 rows of one page
+bool pool_map(CUtensorMap* m, const void* base, const attn::Cache& c, int Hk, int d) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int page = 1 << c.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)Hk, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.row_stride * 2, (cuuint64_t)c.head_stride * 2,
+                                   (cuuint64_t)c.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page, attn::CH_KT), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// query rows of an item: two tiles of whole tokens, at most 128 rows each
+int chunk_rows(int G) { return 2 * (128 / G) * G; }
+
+template <int NB>
+jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o,
+                             void* ws, int Hk, int G, int d, int window, float scale, cudaStream_t s) {
+    typedef attn::ChSmem<NB> SM;
+    const int n_cta = launch_sms(), rows = chunk_rows(G);
+    attn::Work w = make_work(c, b, Hk, G, window, rows, attn::CH_KT, 256, 384);
+    w.tpt = 2 * (128 / G);
+    const attn::Slots sl = make_slots(ws, n_cta, rows, d);
+    CUtensorMap tk, tv;
+    if (!pool_map(&tk, c.k, c, Hk, d) || !pool_map(&tv, c.v, c, Hk, d)) return JET_ERR_CUDA;
+    auto kern = attn::attn_chunk_kernel<NB>;
+    if (smem_attr(kern, SM::BYTES) != JET_OK) return JET_ERR_CUDA;
+    const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv,
+                                 (const __nv_bfloat16*)q, (long long)q_stride, w, sl, (__nv_bfloat16*)o, d,
+                                 scale * 1.44269504f);
+    return st != JET_OK ? st : launch_join(w, sl, o, d, n_cta, s);
+}
+
+// rows per sequence and cache head up to which the decode kernel is taken
+constexpr int kDecodeRows = 32;
+
 }  // namespace
 
 extern "C" {
@@ -169,7 +208,8 @@ size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet
     if (check_attn_shape(AttnShape{nseq, N, 1, 1, 16, Hq, Hk, d, dt}) != JET_OK) return 0;
     if (dt != JET_BF16) return 16;
     const int per_sm = d <= 64 ? attn::DecCfg<64>::CTAS : attn::DecCfg<128>::CTAS;
-    return slot_layout(kMaxSMs * per_sm, attn::DEC_ROWS, d).bytes;
+    return std::max(slot_layout(kMaxSMs * per_sm, attn::DEC_ROWS, d).bytes,
+                    slot_layout(kMaxSMs, chunk_rows(Hq / Hk), d).bytes);
 }
 
 jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
@@ -201,6 +241,10 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
     const attn::Batch b{cu_q, kv_lens, nseq, N};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dt == JET_F32) return launch_attn_simt<float>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s);
+    const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;
+    if (typical * (Hq / Hk) > kDecodeRows)
+        return d <= 64 ? launch_attn_chunk<1>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
+                       : launch_attn_chunk<2>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
     return d <= 64 ? launch_attn_decode<64>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
                    : launch_attn_decode<128>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
 }

@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "k_attn_append.cuh"
+#include "k_attn_chunk.cuh"
 #include "k_attn_common.cuh"
 #include "k_attn_decode.cuh"
 #include "k_attn_sched.cuh"

@@ -1,0 +1,470 @@
+// Attention of a chunk of new tokens per sequence over a paged cache (bf16),
+// on tcgen05: prompt pieces, and batches that mix them with decode tokens.
+//
+// An item is two tiles of 128 query rows (A and B) of one cache head; a row
+// is (token, query head of the group), so all heads that share the cache head
+// are in the same tile and read it once. Per step of 128 positions and tile:
+//   S = Q K^T (fp32, TMEM); P = exp2(scale2 (S - m)) (bf16, over S in TMEM);
+//   O += P V (fp32, TMEM, P as the TMEM operand).
+// The matrix products of a step and tile take about 1024 tensor cycles, its
+// 128 x 128 exponentials 1024 cycles of the SM's special-function unit, so
+// the two tiles alternate: while one is in its softmax the other's products
+// run, and both units are near their limits together.
+//
+//   warps 0-3, 4-7  softmax of tile A, B: one thread per row, the row's 128
+//                   scores in registers, no exchange between threads. The
+//                   maximum m is kept until a score exceeds it by 8 binades
+//                   (weights up to 2^8 are harmless in bf16 and float32), so O
+//                   is rescaled, by the same threads, only then. They also
+//                   load the item's queries and write its results.
+//   warp 8          one thread issues all products
+//   warp 9          one thread issues the TMA loads of K and V: one box per
+//                   page (up to 128 rows), through a ring of 32 KB stages that
+//                   runs ahead into the next item
+//   warp 10         cleans V at the ends of the range (below)
+//
+// Order of the products: S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...
+// S(j+1) overwrites P(j) in TMEM; products of one thread execute in order.
+//
+// A masked weight is exactly zero, but zero times a non-finite value is not.
+// In steps where not every row sees every position, warp 10 zeroes the rows
+// of V outside the item's range (stale memory) and every non-finite value,
+// before the product reads the stage. If it found one inside the range, the
+// rows that do see that value get it added when the results are written.
+//
+// Work is divided as k_attn_sched.cuh says, one CTA to an SM.
+#pragma once
+#include <cuda.h>
+
+#include "k_attn_decode.cuh"
+#include "k_prefill_common.cuh"
+#include "sm100.cuh"
+
+namespace jet {
+namespace attn {
+
+using namespace sm100;
+using pfws::wait_bar;
+
+constexpr int CH_THREADS = 384, CH_KT = 128;
+constexpr int CH_MMA = 256, CH_LOAD = 288, CH_FIX = 320;       // first threads of warps 8, 9, 10
+
+template <int NB> struct ChSmem {                              // NB: 64-column blocks of d
+    static constexpr int STAGES = NB == 2 ? 5 : 8;
+    static constexpr uint32_t TILE = NB * 16384;
+    static constexpr uint32_t Q = 0;                           // [2] tiles
+    static constexpr uint32_t KV = Q + 2 * TILE;               // [STAGES] of K or V
+    static constexpr uint32_t BAR = KV + STAGES * TILE;
+    static constexpr uint32_t MISC = BAR + 384;
+    static constexpr uint32_t BYTES = MISC + 64;
+    static_assert(BYTES <= 232448 - 1024, "shared memory budget (with the static part of block_locate)");
+};
+
+template <int NB> struct ChBar {
+    static constexpr int ST = ChSmem<NB>::STAGES;
+    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, END = O + 2, N = END + 1;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+        :: "r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+// spin a while before sleeping between polls
+__device__ __forceinline__ bool wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    for (int i = 0; i < 4096; ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+    return wait_bar(bar, parity, abort_flag);
+}
+
+// what all roles derive from an item
+struct ChPart {
+    int b0, b1;              // steps of this CTA
+    int p_first;             // position of the first token
+    int lo_all, lo_last;     // first position of the first and of the last token
+    bool two;                // tile B has tokens
+    __device__ __forceinline__ ChPart(const Work& w, const Item& it, long long x0, long long x1) {
+        b0 = it.step_at(x0);
+        b1 = it.step_at(x1);
+        p_first = it.q.L - it.q.n + it.t0;
+        lo_all = first_key(p_first, w.window);
+        lo_last = first_key(it.hi - 1, w.window);
+        two = it.nt > w.tpt / 2;
+    }
+    // not every row sees every position of the step
+    __device__ __forceinline__ bool partial(const Item& it, int step) const {
+        const int k0 = it.lo + step * CH_KT;
+        return k0 < lo_last || k0 + CH_KT > p_first + 1;
+    }
+};
+
+template <int NB>
+__global__ void __launch_bounds__(CH_THREADS, 1)
+attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __nv_bfloat16* __restrict__ q, long long q_stride, const Work w, const Slots sl,
+                  __nv_bfloat16* __restrict__ o, int d, float scale2) {
+    typedef ChSmem<NB> SM;
+    typedef ChBar<NB> B;
+    constexpr int ST = SM::STAGES;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + SM::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::MISC + 16);
+    volatile int* odd_flag = reinterpret_cast<volatile int*>(sm + SM::MISC + 32);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(sm) & 1023u) {                           // whole CTA, before any barrier
+        if (tid == 0) flag_error(DEVERR_DATA);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < B::N; ++i) mbar_init(&bars[i], i >= B::P && i < B::P + 2 ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : 1);
+        *abort_flag = 0;
+        *odd_flag = 0;
+        fence_mbar_init();
+    }
+    if (tid == CH_LOAD) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 0) tmem_alloc(tslot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tslot;
+    pdl_wait();
+    pdl_trigger();
+    long long chunk, total;
+    Item it;
+    const bool inside = block_locate<CH_THREADS>(w, gridDim.x, blockIdx.x, chunk, total, it);
+    const long long x0 = chunk * blockIdx.x, x1 = min(total, x0 + chunk);
+    const int rows = w.tpt / 2 * w.gt;                    // query rows of a tile
+    const int page = 1 << w.c.page_shift;
+
+    if (!inside) {
+        // nothing to do
+    } else if (warp < 8) {
+        // 256 x 200 + 128 x 96 registers of the 384 x 168 that the block starts with
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ------------------------------------------------------------ softmax, queries, results
+        const int tile = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32;
+        const uint32_t tS = taddr_of(tb, lanes, tile * 128), tO = taddr_of(tb, lanes, 256 + tile * 128);
+        uint32_t nS = 0, nO = 0;
+        bool ok = true;
+        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
+            if (it.steps == 0) {                          // every row sees nothing
+                const long long dst = it.a >= x0 && r < rows ? out_row(w, it, tile * rows + r, d) : -1;
+                if (dst >= 0)
+                    for (int e = 0; e < d; e += 8) *reinterpret_cast<uint4*>(o + dst + e) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const ChPart pt(w, it, x0, x1);
+            if (pt.b0 >= pt.b1 || (tile == 1 && !pt.two)) continue;
+            const int hk = it.hh;
+            // the tile's queries: a row's 16-byte pieces across lanes
+            {
+                const int per = d >> 3, t0 = tile * (w.tpt / 2);
+                for (int e = r; e < 128 * per; e += 128) {
+                    const int row = e / per, ch = e - row * per;
+                    const int tok = t0 + row / w.gt, g = row % w.gt;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (row < rows && tok < it.nt)
+                        v = *reinterpret_cast<const uint4*>(q + (it.q.r0 + it.t0 + tok) * q_stride +
+                                                            (long long)(hk * w.G + g) * d + ch * 8);
+                    *reinterpret_cast<uint4*>(sm + SM::Q + tile * SM::TILE + (ch >> 3) * 16384 +
+                                              sw128_off(row, (ch & 7) * 16)) = v;
+                }
+                fence_async_smem();
+                mbar_arrive(&bars[B::Q + tile]);
+            }
+            const int tok = min(tile * (w.tpt / 2) + r / w.gt, it.nt - 1);
+            const int pos = pt.p_first + tok, lo = first_key(pos, w.window);
+            float m = -INFINITY, l = 0.f;
+            for (int step = pt.b0; step < pt.b1; ++step, ++nS) {
+                ok = __all_sync(0xffffffffu, wait_hot(&bars[B::S + tile], nS & 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) tmem_ld32(tS + u * 32, s + u * 32);
+                tmem_ld_wait();
+                if (pt.partial(it, step)) {
+                    const int k0 = it.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > top || c < bot) s[c] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (step == pt.b0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, (top - m) * scale2 > 8.f)) {
+                    // S(step) is complete, so PV(step - 1), issued before it, is too
+                    const float mn = fmaxf(m, top);
+                    const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * scale2);
+                    m = mn;
+                    l *= f;
+                    for (int c = 0; c < d; c += 16) {
+                        uint32_t v[16];
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                                     "%13,%14,%15}, [%16];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                                       "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+                                       "=r"(v[13]), "=r"(v[14]), "=r"(v[15]) : "r"(tO + c));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                                     "%13,%14,%15,%16};"
+                                     :: "r"(tO + c), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                                        "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+                                        "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m * scale2;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float a = ex2(fmaf(__uint_as_float(s[u * 64 + 2 * c]), scale2, -base));
+                        const float b = ex2(fmaf(__uint_as_float(s[u * 64 + 2 * c + 1]), scale2, -base));
+                        sum[c & 3] += a + b;
+                        pk[c] = Vec16<__nv_bfloat16>::pack2(a, b);
+                    }
+                    tmem_st32(tS + u * 32, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B::P + tile]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, wait_hot(&bars[B::O + tile], nO & 1, abort_flag));
+            if (!ok) break;
+            ++nO;
+            tc_fence_after();
+            const bool whole = pt.b0 == 0 && pt.b1 == it.steps;
+            const long long dst = r < rows ? out_row(w, it, tile * rows + r, d) : -1;
+            const long long srow = (long long)(blockIdx.x * 2 + (it.a < x0 ? 0 : 1)) * sl.rows + tile * rows + r;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool odd = *odd_flag != 0;
+            for (int c = 0; c < d; c += 16) {
+                float v[16];
+                uint32_t* u = reinterpret_cast<uint32_t*>(v);
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                             "%13,%14,%15}, [%16];"
+                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+                               "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+                               "=r"(u[13]), "=r"(u[14]), "=r"(u[15]) : "r"(tO + c));
+                tmem_ld_wait();
+                if (odd && dst >= 0) {
+                    // non-finite values that this row sees in the cleaned steps
+                    for (int step = pt.b0; step < pt.b1; ++step) {
+                        if (!pt.partial(it, step)) continue;
+                        const int k0 = it.lo + step * CH_KT;
+                        for (int j = max(k0, lo); j < min(k0 + CH_KT, pos + 1); ++j) {
+                            const int pg = load_page(w.c, it.s, j);
+                            if (pg < 0) continue;
+                            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.c.v) + pg * w.c.page_stride +
+                                                       hk * w.c.head_stride + (j & (page - 1)) * w.c.row_stride + c;
+                            for (int e = 0; e < 16; ++e) {
+                                const float x = __bfloat162float(src[e]);
+                                if (!(fabsf(x) < INFINITY)) v[e] += x;
+                            }
+                        }
+                    }
+                }
+                if (dst < 0) continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= inv;
+                    uint4* to = reinterpret_cast<uint4*>(o + dst + c);
+                    to[0] = Vec16<__nv_bfloat16>::pack(v);
+                    to[1] = Vec16<__nv_bfloat16>::pack(v + 8);
+                } else {
+                    float4* to = reinterpret_cast<float4*>(sl.o + srow * d + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            }
+            if (!whole && dst >= 0) sl.ml[srow] = make_float2(m * scale2, l);
+            // the loads of O above are complete (waited for); the next item's products may
+            // overwrite it once this thread has let them
+            tc_fence_before();
+        }
+        if (!ok) *abort_flag = 1;
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (tid == CH_MMA) {
+        // ------------------------------------------------------------ products
+        const uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, d, false, true);
+        const uint64_t dQ = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
+        const uint64_t dK = sw128_desc(smem_u32(sm + SM::KV), 16, 1024);
+        const uint64_t dV = sw128_desc(smem_u32(sm + SM::KV), 16384, 1024);
+        const int ks = d >> 4;
+        uint32_t kv = 0, fix = 0, nQ[2] = {0, 0}, nP[2] = {0, 0};
+        bool ok = true;
+        auto full = [&](uint32_t i) { return wait_hot(&bars[B::FULL + i % ST], (i / ST) & 1, abort_flag); };
+        auto issue_s = [&](int tile, uint32_t slot) {
+            for (int k = 0; k < ks; ++k) {
+                const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                mma_bf16_ss(tb + tile * 128, dQ + (tile * SM::TILE >> 4) + off, dK + (slot * SM::TILE >> 4) + off, id_s, k > 0);
+            }
+            mma_commit(&bars[B::S + tile]);
+        };
+        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
+            const ChPart pt(w, it, x0, x1);
+            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+            const int tiles = pt.two ? 2 : 1;
+            ok = full(kv);
+            for (int i = 0; i < tiles && ok; ++i) {
+                ok = wait_hot(&bars[B::Q + i], nQ[i]++ & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(i, kv % ST);
+            }
+            if (!ok) break;
+            mma_commit(&bars[B::EMPTY + kv % ST]);
+            ++kv;
+            for (int step = pt.b0; step < pt.b1 && ok; ++step) {
+                const bool more = step + 1 < pt.b1;
+                const uint32_t vs = kv % ST;
+                ok = full(kv);
+                if (ok && pt.partial(it, step)) {
+                    ok = wait_hot(&bars[B::FIX + vs], fix >> vs & 1, abort_flag);
+                    fix ^= 1u << vs;
+                }
+                for (int i = 0; i < tiles && ok; ++i) {
+                    ok = wait_hot(&bars[B::P + i], nP[i]++ & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < CH_KT / 16; ++k)
+                        mma_bf16_ts(tb + 256 + i * 128, tb + i * 128 + k * 8, dV + ((vs * SM::TILE + k * 2048) >> 4), id_o,
+                                    step > pt.b0 || k > 0);
+                    if (i == tiles - 1) mma_commit(&bars[B::EMPTY + vs]);
+                    if (!more) {
+                        mma_commit(&bars[B::O + i]);
+                        continue;
+                    }
+                    if (i == 0) {
+                        ok = full(kv + 1);
+                        if (!ok) break;
+                    }
+                    issue_s(i, (kv + 1) % ST);
+                    if (i == tiles - 1) mma_commit(&bars[B::EMPTY + (kv + 1) % ST]);
+                }
+                kv += more ? 2 : 1;
+            }
+        }
+        if (!ok) *abort_flag = 1;
+        // every product has completed before the CTA frees its memory
+        mma_commit(&bars[B::END]);
+        mbar_wait(&bars[B::END], 0);
+    } else if (tid == CH_LOAD) {
+        // ------------------------------------------------------------ loads
+        uint32_t kv = 0;
+        bool ok = true;
+        const int box = min(page, CH_KT);
+        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
+            const ChPart pt(w, it, x0, x1);
+            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+            for (int step = pt.b0; step < pt.b1 && ok; ++step) {
+                const int k0 = it.lo + step * CH_KT;
+                // boxes of the step that hold positions of the range
+                const int e0 = max(0, pt.lo_all - k0) / box, e1 = (min(CH_KT, it.hi - k0) + box - 1) / box;
+                for (int v = 0; v < 2 && ok; ++v, ++kv) {
+                    const uint32_t slot = kv % ST;
+                    if (kv >= ST) ok = wait_bar(&bars[B::EMPTY + slot], (kv / ST - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    uint64_t* bar = &bars[B::FULL + slot];
+                    mbar_expect_tx(bar, (uint32_t)(e1 - e0) * box * 128 * NB);
+                    uint8_t* dst = sm + SM::KV + slot * SM::TILE;
+                    for (int e = e0; e < e1; ++e) {
+                        const int p = k0 + e * box;
+                        int pg = load_page(w.c, it.s, p);
+                        if (pg < 0) pg = w.c.n_pages;                     // behind the pool: reads zeros
+#pragma unroll
+                        for (int c = 0; c < NB; ++c)
+                            tma_load_4d(dst + c * 16384 + e * box * 128, v ? &tm_v : &tm_k, bar, c * 64, p & (page - 1),
+                                        it.hh, pg);
+                    }
+                }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+        // every issued load has landed before the CTA frees its memory
+        for (uint32_t i = kv > ST ? kv - ST : 0; i < kv; ++i) mbar_wait(&bars[B::FULL + i % ST], (i / ST) & 1);
+    } else if (tid >= CH_FIX && tid < CH_FIX + 32) {
+        // ------------------------------------------------------------ V at the ends of the range
+        uint32_t kv = 0;
+        bool ok = true;
+        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
+            const ChPart pt(w, it, x0, x1);
+            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+            for (int step = pt.b0; step < pt.b1 && ok; ++step, kv += 2) {
+                // every stage in its turn: a wait that skipped one could take an older phase for its own
+                const uint32_t vi = kv + 1, slot = vi % ST;
+                ok = wait_bar(&bars[B::FULL + kv % ST], (kv / ST) & 1, abort_flag) &&
+                     wait_bar(&bars[B::FULL + slot], (vi / ST) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (!pt.partial(it, step)) continue;
+                const int k0 = it.lo + step * CH_KT;
+                uint8_t* V = sm + SM::KV + slot * SM::TILE;
+                bool odd = false;
+#pragma unroll 8
+                for (int u = 0; u < NB * 32; ++u) {
+                    const int row = (u % 32) * 4 + (lane >> 3);
+                    uint4* at = reinterpret_cast<uint4*>(V + (u / 32) * 16384 + row * 128 + (lane & 7) * 16);
+                    const bool out = k0 + row < pt.lo_all || k0 + row >= it.hi;
+                    uint4 x = *at;
+                    const bool bad = nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
+                    if (out) {
+                        *at = make_uint4(0, 0, 0, 0);
+                    } else if (bad) {
+                        odd = true;
+                        uint32_t* h = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((h[e] & 0x7f80u) == 0x7f80u) h[e] &= 0xffff0000u;
+                            if ((h[e] & 0x7f800000u) == 0x7f800000u) h[e] &= 0xffffu;
+                        }
+                        *at = x;
+                    }
+                }
+                if (odd) *odd_flag = 1;
+                __threadfence_block();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B::FIX + slot]);
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tb, 512);
+}
+
+}  // namespace attn
+}  // namespace jet
