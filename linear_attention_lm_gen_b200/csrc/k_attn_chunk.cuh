@@ -17,10 +17,10 @@
 //                   (weights up to 2^8 are harmless in bf16 and float32), so O
 //                   is rescaled, by the same threads, only then. They also
 //                   load the item's queries and write its results.
-//   warp 8          one thread issues all products
-//   warp 9          one thread issues the TMA loads of K and V: one box per
-//                   page (up to 128 rows), through a ring of 32 KB stages that
-//                   runs ahead into the next item
+//   warp 8          one lane issues all products
+//   warp 9          the TMA loads of K and V, one box per page (up to 128
+//                   rows) and lane, page indices a step ahead, through a ring of
+//                   32 KB stages that runs ahead into the next item
 //   warp 10         cleans V at the ends of the range (below)
 //
 // Order of the products: S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...
@@ -81,6 +81,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 // spin a while before sleeping between polls
 __device__ __forceinline__ bool wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -312,106 +317,143 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (!ok) *abort_flag = 1;
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (tid == CH_MMA) {
-        // ------------------------------------------------------------ products
+    if (warp == CH_MMA / 32) {
+        // ------------------------------------------------------------ products: the warp waits as one, one
+        // elected lane issues
         const uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, d, false, true);
         const uint64_t dQ = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
         const uint64_t dK = sw128_desc(smem_u32(sm + SM::KV), 16, 1024);
         const uint64_t dV = sw128_desc(smem_u32(sm + SM::KV), 16384, 1024);
         const int ks = d >> 4;
-        uint32_t kv = 0, fix = 0, nQ[2] = {0, 0}, nP[2] = {0, 0};
+        const bool one = elect_one();
+        // ring position (stage, phase) of the next K or V, and the phases of the other barriers
+        uint32_t slot = 0, ph = 0, fix = 0, phQ[2] = {0, 0}, phP[2] = {0, 0};
         bool ok = true;
-        auto full = [&](uint32_t i) { return wait_hot(&bars[B::FULL + i % ST], (i / ST) & 1, abort_flag); };
-        auto issue_s = [&](int tile, uint32_t slot) {
-            for (int k = 0; k < ks; ++k) {
-                const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                mma_bf16_ss(tb + tile * 128, dQ + (tile * SM::TILE >> 4) + off, dK + (slot * SM::TILE >> 4) + off, id_s, k > 0);
+        auto wait = [&](int bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, wait_hot(&bars[bar], parity, abort_flag));
+            return ok;
+        };
+        auto advance = [&]() {
+            if (++slot == ST) { slot = 0; ph ^= 1; }
+        };
+        auto issue_s = [&](int tile, uint32_t sl_) {
+            if (one) {
+                const uint64_t a = dQ + (tile * SM::TILE >> 4), b = dK + (sl_ * SM::TILE >> 4);
+#pragma unroll
+                for (int k = 0; k < NB * 4; ++k)
+                    if (k < ks) {
+                        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        mma_bf16_ss(tb + tile * 128, a + off, b + off, id_s, k > 0);
+                    }
+                mma_commit(&bars[B::S + tile]);
             }
-            mma_commit(&bars[B::S + tile]);
+            __syncwarp();
+        };
+        auto issue_o = [&](int tile, uint32_t sl_, bool fresh) {
+            if (one) {
+                const uint64_t b = dV + (sl_ * SM::TILE >> 4);
+#pragma unroll
+                for (int k = 0; k < CH_KT / 16; ++k)
+                    mma_bf16_ts(tb + 256 + tile * 128, tb + tile * 128 + k * 8, b + (k * 2048 >> 4), id_o, !fresh || k > 0);
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t bar) {
+            if (one) mma_commit(&bars[bar]);
+            __syncwarp();
         };
         for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
             const ChPart pt(w, it, x0, x1);
             if (it.steps == 0 || pt.b0 >= pt.b1) continue;
-            const int tiles = pt.two ? 2 : 1;
-            ok = full(kv);
-            for (int i = 0; i < tiles && ok; ++i) {
-                ok = wait_hot(&bars[B::Q + i], nQ[i]++ & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                issue_s(i, kv % ST);
-            }
+            if (!wait(B::FULL + slot, ph)) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (i == 0 || pt.two) {
+                    if (wait(B::Q + i, phQ[i])) {
+                        phQ[i] ^= 1;
+                        tc_fence_after();
+                        issue_s(i, slot);
+                    }
+                }
             if (!ok) break;
-            mma_commit(&bars[B::EMPTY + kv % ST]);
-            ++kv;
+            release(B::EMPTY + slot);
+            advance();
             for (int step = pt.b0; step < pt.b1 && ok; ++step) {
-                const bool more = step + 1 < pt.b1;
-                const uint32_t vs = kv % ST;
-                ok = full(kv);
-                if (ok && pt.partial(it, step)) {
-                    ok = wait_hot(&bars[B::FIX + vs], fix >> vs & 1, abort_flag);
+                const bool more = step + 1 < pt.b1, fresh = step == pt.b0;
+                const uint32_t vs = slot;
+                wait(B::FULL + vs, ph);
+                if (pt.partial(it, step)) {
+                    wait(B::FIX + vs, fix >> vs & 1);
                     fix ^= 1u << vs;
                 }
-                for (int i = 0; i < tiles && ok; ++i) {
-                    ok = wait_hot(&bars[B::P + i], nP[i]++ & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
+                advance();
 #pragma unroll
-                    for (int k = 0; k < CH_KT / 16; ++k)
-                        mma_bf16_ts(tb + 256 + i * 128, tb + i * 128 + k * 8, dV + ((vs * SM::TILE + k * 2048) >> 4), id_o,
-                                    step > pt.b0 || k > 0);
-                    if (i == tiles - 1) mma_commit(&bars[B::EMPTY + vs]);
+                for (int i = 0; i < 2; ++i) {
+                    if ((i == 1 && !pt.two) || !wait(B::P + i, phP[i])) break;
+                    phP[i] ^= 1;
+                    tc_fence_after();
+                    issue_o(i, vs, fresh);
+                    const bool final = i == 1 || !pt.two;
+                    if (final) release(B::EMPTY + vs);
                     if (!more) {
-                        mma_commit(&bars[B::O + i]);
-                        continue;
+                        release(B::O + i);
+                    } else {
+                        if (i == 0 && !wait(B::FULL + slot, ph)) break;
+                        issue_s(i, slot);
+                        if (final) release(B::EMPTY + slot);
                     }
-                    if (i == 0) {
-                        ok = full(kv + 1);
-                        if (!ok) break;
-                    }
-                    issue_s(i, (kv + 1) % ST);
-                    if (i == tiles - 1) mma_commit(&bars[B::EMPTY + (kv + 1) % ST]);
                 }
-                kv += more ? 2 : 1;
+                if (more) advance();
             }
         }
         if (!ok) *abort_flag = 1;
         // every product has completed before the CTA frees its memory
-        mma_commit(&bars[B::END]);
-        mbar_wait(&bars[B::END], 0);
-    } else if (tid == CH_LOAD) {
-        // ------------------------------------------------------------ loads
+        if (one) {
+            mma_commit(&bars[B::END]);
+            mbar_wait(&bars[B::END], 0);
+        }
+    } else if (warp == CH_LOAD / 32) {
+        // ------------------------------------------------------------ loads: lane e issues box e of a step
         uint32_t kv = 0;
         bool ok = true;
         const int box = min(page, CH_KT);
         for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
             const ChPart pt(w, it, x0, x1);
             if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+            // this lane's page of a step, or -1: no positions of the range in its box
+            auto fetch = [&](int step) -> int {
+                const int k0 = it.lo + step * CH_KT, p = k0 + lane * box;
+                if (step >= pt.b1 || lane * box >= CH_KT || p >= it.hi || p + box <= pt.lo_all) return -1;
+                const int pg = load_page(w.c, it.s, p);
+                return pg < 0 ? w.c.n_pages : pg;                 // a bad index: behind the pool, reads zeros
+            };
+            int pg = fetch(pt.b0);
             for (int step = pt.b0; step < pt.b1 && ok; ++step) {
-                const int k0 = it.lo + step * CH_KT;
-                // boxes of the step that hold positions of the range
-                const int e0 = max(0, pt.lo_all - k0) / box, e1 = (min(CH_KT, it.hi - k0) + box - 1) / box;
-                for (int v = 0; v < 2 && ok; ++v, ++kv) {
+                const int next = fetch(step + 1);
+                const int p = it.lo + step * CH_KT + lane * box;
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box * 128 * NB;
+                for (int v = 0; v < 2; ++v, ++kv) {
                     const uint32_t slot = kv % ST;
-                    if (kv >= ST) ok = wait_bar(&bars[B::EMPTY + slot], (kv / ST - 1) & 1, abort_flag);
-                    if (!ok) break;
                     uint64_t* bar = &bars[B::FULL + slot];
-                    mbar_expect_tx(bar, (uint32_t)(e1 - e0) * box * 128 * NB);
-                    uint8_t* dst = sm + SM::KV + slot * SM::TILE;
-                    for (int e = e0; e < e1; ++e) {
-                        const int p = k0 + e * box;
-                        int pg = load_page(w.c, it.s, p);
-                        if (pg < 0) pg = w.c.n_pages;                     // behind the pool: reads zeros
+                    if (lane == 0) {
+                        if (kv >= ST) ok = wait_hot(&bars[B::EMPTY + slot], (kv / ST - 1) & 1, abort_flag);
+                        if (ok) mbar_expect_tx(bar, bytes);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* dst = sm + SM::KV + slot * SM::TILE + lane * box * 128;
+                    if (pg >= 0)
 #pragma unroll
                         for (int c = 0; c < NB; ++c)
-                            tma_load_4d(dst + c * 16384 + e * box * 128, v ? &tm_v : &tm_k, bar, c * 64, p & (page - 1),
-                                        it.hh, pg);
-                    }
+                            tma_load_4d(dst + c * 16384, v ? &tm_v : &tm_k, bar, c * 64, p & (page - 1), it.hh, pg);
                 }
+                pg = next;
             }
         }
         if (!ok) *abort_flag = 1;
         // every issued load has landed before the CTA frees its memory
-        for (uint32_t i = kv > ST ? kv - ST : 0; i < kv; ++i) mbar_wait(&bars[B::FULL + i % ST], (i / ST) & 1);
+        if (lane == 0)
+            for (uint32_t i = kv > ST ? kv - ST : 0; i < kv; ++i) mbar_wait(&bars[B::FULL + i % ST], (i / ST) & 1);
     } else if (tid >= CH_FIX && tid < CH_FIX + 32) {
         // ------------------------------------------------------------ V at the ends of the range
         uint32_t kv = 0;
