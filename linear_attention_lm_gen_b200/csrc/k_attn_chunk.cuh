@@ -62,15 +62,69 @@ template <int NB> struct ChSmem {                              // NB: 64-column 
 
 template <int NB> struct ChBar {
     static constexpr int ST = ChSmem<NB>::STAGES;
-    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, END = O + 2, N = END + 1;
+    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, R = O + 2, END = R + 2, N = END + 1;
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A * B[smem], A in shared memory or in TMEM, where `one` holds.
+// The lane is chosen inside the instruction, so that the code around it stays
+// uniform and its addresses in uniform registers.
+__device__ __forceinline__ void mma_ss_if(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-        :: "r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+        :: "r"(smem_u32(bar)), "r"(one) : "memory");
+}
+// 32 lanes x 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// packed float32 arithmetic on pairs, and the largest of three
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int x, int y, int z, int w) {
     asm volatile(
@@ -134,7 +188,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < B::N; ++i) mbar_init(&bars[i], i >= B::P && i < B::P + 2 ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : 1);
+        for (int i = 0; i < B::N; ++i) {
+            const bool warps = (i >= B::P && i < B::P + 2) || (i >= B::R && i < B::R + 2);    // one arrival per warp
+            mbar_init(&bars[i], warps ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : 1);
+        }
         *abort_flag = 0;
         *odd_flag = 0;
         fence_mbar_init();
@@ -177,19 +234,34 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
             const ChPart pt(w, it, x0, x1);
             if (pt.b0 >= pt.b1 || (tile == 1 && !pt.two)) continue;
-            const int hk = it.hh;
-            // the tile's queries: a row's 16-byte pieces across lanes
+            // the tile's queries, eight 16-byte pieces of rows in flight per
+            // thread; x / n = x * (65536 / n + 1) >> 16 for the small x and n here
+            if (nO > 0) {                       // the last item's results have left the buffer
+                ok = __all_sync(0xffffffffu, wait_hot(&bars[B::R + tile], (nO - 1) & 1, abort_flag));
+                if (!ok) break;
+            }
             {
                 const int per = d >> 3, t0 = tile * (w.tpt / 2);
-                for (int e = r; e < 128 * per; e += 128) {
-                    const int row = e / per, ch = e - row * per;
-                    const int tok = t0 + row / w.gt, g = row % w.gt;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < rows && tok < it.nt)
-                        v = *reinterpret_cast<const uint4*>(q + (it.q.r0 + it.t0 + tok) * q_stride +
-                                                            (long long)(hk * w.G + g) * d + ch * 8);
-                    *reinterpret_cast<uint4*>(sm + SM::Q + tile * SM::TILE + (ch >> 3) * 16384 +
-                                              sw128_off(row, (ch & 7) * 16)) = v;
+                const uint32_t mper = 65536 / per + 1, mgt = 65536 / w.gt + 1;
+                const __nv_bfloat16* qb = q + (it.q.r0 + it.t0 + t0) * q_stride + (long long)(it.hh * w.G) * d;
+                uint8_t* to = sm + SM::Q + tile * SM::TILE;
+#pragma unroll 1
+                for (int e0 = r; e0 < 128 * per; e0 += 128 * 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int e = e0 + u * 128, row = (int)(e * mper >> 16), ch = e - row * per;
+                        const int tok = (int)(row * mgt >> 16), g = row - tok * w.gt;
+                        v[u] = make_uint4(0, 0, 0, 0);
+                        if (row < rows && t0 + tok < it.nt)
+                            v[u] = *reinterpret_cast<const uint4*>(qb + tok * q_stride + g * d + ch * 8);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int e = e0 + u * 128, row = (int)(e * mper >> 16), ch = e - row * per;
+                        if (row < 128)
+                            *reinterpret_cast<uint4*>(to + (ch >> 3) * 16384 + sw128_off(row, (ch & 7) * 16)) = v[u];
+                    }
                 }
                 fence_async_smem();
                 mbar_arrive(&bars[B::Q + tile]);
@@ -201,20 +273,35 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 ok = __all_sync(0xffffffffu, wait_hot(&bars[B::S + tile], nS & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
+                if (pt.partial(it, step)) {              // masked scores become -inf in place
+                    const int k0 = it.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(tS + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e > top || c + e < bot) v[e] = 0xff800000u;
+                        tmem_st16(tS + c, v);
+                    }
+                    tmem_st_wait();
+                }
                 uint32_t s[128];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) tmem_ld32(tS + u * 32, s + u * 32);
                 tmem_ld_wait();
-                if (pt.partial(it, step)) {
-                    const int k0 = it.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
+                float mx[4];
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > top || c < bot) s[c] = 0xff800000u;
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
 #pragma unroll
-                for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[124 + e]));
+                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                 if (step == pt.b0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, (top - m) * scale2 > 8.f)) {
@@ -223,38 +310,40 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * scale2);
                     m = mn;
                     l *= f;
+#pragma unroll 1
                     for (int c = 0; c < d; c += 16) {
                         uint32_t v[16];
-                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-                                     "%13,%14,%15}, [%16];"
-                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-                                       "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-                                       "=r"(v[13]), "=r"(v[14]), "=r"(v[15]) : "r"(tO + c));
+                        tmem_ld16(tO + c, v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-                                     "%13,%14,%15,%16};"
-                                     :: "r"(tO + c), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-                                        "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
-                                        "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+                        tmem_st16(tO + c, v);
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : m * scale2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pair(scale2, scale2), nb2 = pair(-base, -base);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t pk[32];
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float a = ex2(fmaf(__uint_as_float(s[u * 64 + 2 * c]), scale2, -base));
-                        const float b = ex2(fmaf(__uint_as_float(s[u * 64 + 2 * c + 1]), scale2, -base));
-                        sum[c & 3] += a + b;
+                    for (int c = 0; c < 16; ++c) {
+                        const uint64_t x = fma2(pair(__uint_as_float(s[u * 32 + 2 * c]), __uint_as_float(s[u * 32 + 2 * c + 1])),
+                                                sc2, nb2);
+                        float a, b;
+                        unpair(x, a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[c & 3] = add2(sum[c & 3], pair(a, b));
                         pk[c] = Vec16<__nv_bfloat16>::pack2(a, b);
                     }
-                    tmem_st32(tS + u * 32, pk);
+                    tmem_st16(tS + u * 16, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                {
+                    float a, b;
+                    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                    l += a + b;
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -269,50 +358,81 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const long long dst = r < rows ? out_row(w, it, tile * rows + r, d) : -1;
             const long long srow = (long long)(blockIdx.x * 2 + (it.a < x0 ? 0 : 1)) * sl.rows + tile * rows + r;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool odd = *odd_flag != 0;
-            for (int c = 0; c < d; c += 16) {
-                float v[16];
-                uint32_t* u = reinterpret_cast<uint32_t*>(v);
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-                             "%13,%14,%15}, [%16];"
-                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-                               "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
-                               "=r"(u[13]), "=r"(u[14]), "=r"(u[15]) : "r"(tO + c));
-                tmem_ld_wait();
-                if (odd && dst >= 0) {
-                    // non-finite values that this row sees in the cleaned steps
-                    for (int step = pt.b0; step < pt.b1; ++step) {
+            if (*odd_flag) {
+                // values that were cleaned out of V: a row gets the non-finite ones that it sees
+#pragma unroll 1
+                for (int c = 0; c < d; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tO + c, v);
+                    tmem_ld_wait();
+                    for (int step = pt.b0; step < pt.b1 && dst >= 0; ++step) {
                         if (!pt.partial(it, step)) continue;
                         const int k0 = it.lo + step * CH_KT;
                         for (int j = max(k0, lo); j < min(k0 + CH_KT, pos + 1); ++j) {
                             const int pg = load_page(w.c, it.s, j);
                             if (pg < 0) continue;
                             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.c.v) + pg * w.c.page_stride +
-                                                       hk * w.c.head_stride + (j & (page - 1)) * w.c.row_stride + c;
+                                                       it.hh * w.c.head_stride + (j & (page - 1)) * w.c.row_stride + c;
+#pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const float x = __bfloat162float(src[e]);
-                                if (!(fabsf(x) < INFINITY)) v[e] += x;
+                                if (!(fabsf(x) < INFINITY)) v[e] = __float_as_uint(__uint_as_float(v[e]) + x);
                             }
                         }
                     }
+                    __syncwarp();
+                    tmem_st16(tO + c, v);
+                    tmem_st_wait();
                 }
-                if (dst < 0) continue;
+            }
+            // 32 columns at a time: rows to shared memory (the queries' buffer, free
+            // once O is complete), then out with consecutive lanes on a row
+            uint8_t* stage = sm + SM::Q + tile * SM::TILE + (warp & 3) * 4096;
+            const long long out = whole ? dst : dst < 0 ? -1 : srow * d;
+#pragma unroll 1
+            for (int c = 0; c < d; c += 32) {
+                float v[32];
+                tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(v));
+                tmem_ld_wait();
+                const int nc = min(32, d - c);
                 if (whole) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] *= inv;
-                    uint4* to = reinterpret_cast<uint4*>(o + dst + c);
-                    to[0] = Vec16<__nv_bfloat16>::pack(v);
-                    to[1] = Vec16<__nv_bfloat16>::pack(v + 8);
-                } else {
-                    float4* to = reinterpret_cast<float4*>(sl.o + srow * d + c);
+                    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        for (int k = 0; k < 8; ++k) v[e * 8 + k] *= inv;
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
+                            Vec16<__nv_bfloat16>::pack(v + e * 8);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = k * 8 + (lane >> 2), ch = lane & 3;
+                        const long long to = __shfl_sync(0xffffffffu, out, row);
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + ((ch ^ (row >> 1 & 3)) << 4));
+                        if (to >= 0 && ch * 8 < nc) *reinterpret_cast<uint4*>(o + to + c + ch * 8) = x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = k * 4 + (lane >> 3), ch = lane & 7;
+                        const long long to = __shfl_sync(0xffffffffu, out, row);
+                        const float4 x = *reinterpret_cast<const float4*>(stage + row * 128 + ((ch ^ (row & 7)) << 4));
+                        if (to >= 0 && ch * 4 < nc) *reinterpret_cast<float4*>(sl.o + to + c + ch * 4) = x;
+                    }
                 }
+                __syncwarp();
             }
             if (!whole && dst >= 0) sl.ml[srow] = make_float2(m * scale2, l);
             // the loads of O above are complete (waited for); the next item's products may
             // overwrite it once this thread has let them
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B::R + tile]);
         }
         if (!ok) *abort_flag = 1;
     } else {
@@ -325,7 +445,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint64_t dK = sw128_desc(smem_u32(sm + SM::KV), 16, 1024);
         const uint64_t dV = sw128_desc(smem_u32(sm + SM::KV), 16384, 1024);
         const int ks = d >> 4;
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         // ring position (stage, phase) of the next K or V, and the phases of the other barriers
         uint32_t slot = 0, ph = 0, fix = 0, phQ[2] = {0, 0}, phP[2] = {0, 0};
         bool ok = true;
@@ -337,31 +457,22 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (++slot == ST) { slot = 0; ph ^= 1; }
         };
         auto issue_s = [&](int tile, uint32_t sl_) {
-            if (one) {
-                const uint64_t a = dQ + (tile * SM::TILE >> 4), b = dK + (sl_ * SM::TILE >> 4);
+            const uint64_t a = dQ + (tile * SM::TILE >> 4), b = dK + (sl_ * SM::TILE >> 4);
 #pragma unroll
-                for (int k = 0; k < NB * 4; ++k)
-                    if (k < ks) {
-                        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        mma_bf16_ss(tb + tile * 128, a + off, b + off, id_s, k > 0);
-                    }
-                mma_commit(&bars[B::S + tile]);
-            }
-            __syncwarp();
+            for (int k = 0; k < NB * 4; ++k)
+                if (k < ks) {
+                    const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    mma_ss_if(one, tb + tile * 128, a + off, b + off, id_s, k > 0);
+                }
+            commit_if(one, &bars[B::S + tile]);
         };
         auto issue_o = [&](int tile, uint32_t sl_, bool fresh) {
-            if (one) {
-                const uint64_t b = dV + (sl_ * SM::TILE >> 4);
+            const uint64_t b = dV + (sl_ * SM::TILE >> 4);
 #pragma unroll
-                for (int k = 0; k < CH_KT / 16; ++k)
-                    mma_bf16_ts(tb + 256 + tile * 128, tb + tile * 128 + k * 8, b + (k * 2048 >> 4), id_o, !fresh || k > 0);
-            }
-            __syncwarp();
+            for (int k = 0; k < CH_KT / 16; ++k)
+                mma_ts_if(one, tb + 256 + tile * 128, tb + tile * 128 + k * 8, b + (k * 2048 >> 4), id_o, !fresh || k > 0);
         };
-        auto release = [&](uint32_t bar) {
-            if (one) mma_commit(&bars[bar]);
-            __syncwarp();
-        };
+        auto release = [&](uint32_t bar) { commit_if(one, &bars[bar]); };
         for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
             const ChPart pt(w, it, x0, x1);
             if (it.steps == 0 || pt.b0 >= pt.b1) continue;
@@ -387,20 +498,18 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     fix ^= 1u << vs;
                 }
                 advance();
+                if (more) wait(B::FULL + slot, ph);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if ((i == 1 && !pt.two) || !wait(B::P + i, phP[i])) break;
                     phP[i] ^= 1;
                     tc_fence_after();
                     issue_o(i, vs, fresh);
-                    const bool final = i == 1 || !pt.two;
-                    if (final) release(B::EMPTY + vs);
-                    if (!more) {
-                        release(B::O + i);
-                    } else {
-                        if (i == 0 && !wait(B::FULL + slot, ph)) break;
-                        issue_s(i, slot);
-                        if (final) release(B::EMPTY + slot);
+                    if (more) issue_s(i, slot);
+                    else release(B::O + i);
+                    if (i == 1 || !pt.two) {
+                        release(B::EMPTY + vs);
+                        if (more) release(B::EMPTY + slot);
                     }
                 }
                 if (more) advance();

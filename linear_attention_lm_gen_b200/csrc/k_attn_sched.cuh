@@ -35,8 +35,9 @@ struct Work {
 __device__ __forceinline__ long long tiles_cost(const Work& w, long long A, long long i) {
     long long m = i;
     if (w.window > 0) {
-        const long long first = (w.window - 1 - A + w.tpt - 1) / w.tpt;      // first tile the window cuts
-        m = min(i, max(0LL, first));
+        // first tile that the window cuts (A and the window are below 2^31)
+        const unsigned ahead = A < w.window - 1 ? (unsigned)(w.window - 1 - A) : 0u;
+        m = min(i, (long long)((ahead + w.tpt - 1) / w.tpt));
     }
     return m * (w.c0 + A) + w.tpt * (m * (m + 1) / 2) + (i - m) * ((long long)w.c0 + w.tpt + w.window - 1);
 }
@@ -65,11 +66,12 @@ struct Item {
         hi = p0 + nt;
         steps = hi > lo ? (hi - lo + w.kt - 1) / w.kt : 0;
     }
-    // first step at or behind place x of the axis
+    // first step at or behind place x of the axis. In float64: any monotone
+    // function of x serves, as long as every caller computes the same.
     __device__ __forceinline__ int step_at(long long x) const {
         if (x <= a) return 0;
         if (x >= a + cost) return steps;
-        return (int)((x - a) * steps / cost);
+        return min(steps, (int)((double)(x - a) * (double)steps / (double)cost));
     }
     __device__ __forceinline__ void next(const Work& w) {
         a += cost;
@@ -127,8 +129,10 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
             const Seq q = load_seq(w.b, w.c, s, false);
             const long long cost = q.n > 0 ? seq_cost(w, q) : 0;
             if (x < before + cost) {
-                const long long A = max(0, q.L - q.n), per_head = cost / (w.Hk * w.hs);
-                const long long hh = (x - before) / per_head, rem = (x - before) - hh * per_head;
+                const long long A = max(0, q.L - q.n), per_head = tiles_cost(w, A, seq_tiles(w, q));
+                int hh = 0;
+                long long rem = x - before;
+                for (; rem >= per_head; ++hh) rem -= per_head;
                 int lo = 0, hi = seq_tiles(w, q) - 1;          // largest tile that starts at or before rem
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
@@ -136,7 +140,7 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
                     else hi = mid - 1;
                 }
                 found[0] = s;
-                found[1] = (int)hh;
+                found[1] = hh;
                 found[2] = lo;
                 found_a = before + hh * per_head + tiles_cost(w, A, lo);
                 break;
