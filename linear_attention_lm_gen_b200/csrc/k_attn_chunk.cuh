@@ -22,6 +22,11 @@
 //                   rows) and lane, page indices a step ahead, through a ring of
 //                   32 KB stages that runs ahead into the next item
 //   warp 10         cleans V at the ends of the range (below)
+//   warp 11         one lane walks the axis of the work and hands the items to
+//                   the other roles through a queue of four, so that the walk's
+//                   64-bit arithmetic exists once (inlined into every role it made
+//                   the kernel 190 KB long, and each switch of items waited for
+//                   instructions)
 //
 // Order of the products: S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...
 // S(j+1) overwrites P(j) in TMEM; products of one thread execute in order.
@@ -37,17 +42,15 @@
 #include <cuda.h>
 
 #include "k_attn_decode.cuh"
-#include "k_prefill_common.cuh"
 #include "sm100.cuh"
 
 namespace jet {
 namespace attn {
 
 using namespace sm100;
-using pfws::wait_bar;
 
 constexpr int CH_THREADS = 384, CH_KT = 128;
-constexpr int CH_MMA = 256, CH_LOAD = 288, CH_FIX = 320;       // first threads of warps 8, 9, 10
+constexpr int CH_MMA = 256, CH_LOAD = 288, CH_FIX = 320, CH_WALK = 352;       // first threads of warps 8 to 11
 
 template <int NB> struct ChSmem {                              // NB: 64-column blocks of d
     static constexpr int STAGES = NB == 2 ? 5 : 8;
@@ -56,13 +59,14 @@ template <int NB> struct ChSmem {                              // NB: 64-column 
     static constexpr uint32_t KV = Q + 2 * TILE;               // [STAGES] of K or V
     static constexpr uint32_t BAR = KV + STAGES * TILE;
     static constexpr uint32_t MISC = BAR + 384;
-    static constexpr uint32_t BYTES = MISC + 64;
+    static constexpr uint32_t ITEMS = MISC + 64;               // [4] of the item queue
+    static constexpr uint32_t BYTES = ITEMS + 4 * 48;
     static_assert(BYTES <= 232448 - 1024, "shared memory budget (with the static part of block_locate)");
 };
 
 template <int NB> struct ChBar {
     static constexpr int ST = ChSmem<NB>::STAGES;
-    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, R = O + 2, END = R + 2, N = END + 1;
+    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, R = O + 2, END = R + 2, IF = END + 1, IE = IF + 4, N = IE + 4;
 };
 
 // D[tmem] (+)= A * B[smem], A in shared memory or in TMEM, where `one` holds.
@@ -141,33 +145,37 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-// spin a while before sleeping between polls
-__device__ __forceinline__ bool wait_hot(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    for (int i = 0; i < 4096; ++i)
-        if (mbar_test_wait(bar, parity)) return true;
-    return wait_bar(bar, parity, abort_flag);
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;        // suspends the thread for a while by itself
+        if ((i & 15u) == 0) {
+            if (*abort_flag) return false;
+            if (global_ns() - t0 > kWaitLimitNs) break;
+        }
+    }
+    *abort_flag = 1;
+    flag_error(DEVERR_TIMEOUT);
+    return false;
+}
+// Wait for a phase, bounded in time; false once any role gave up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag);
 }
 
-// what all roles derive from an item
-struct ChPart {
-    int b0, b1;              // steps of this CTA
-    int p_first;             // position of the first token
-    int lo_all, lo_last;     // first position of the first and of the last token
-    bool two;                // tile B has tokens
-    __device__ __forceinline__ ChPart(const Work& w, const Item& it, long long x0, long long x1) {
-        b0 = it.step_at(x0);
-        b1 = it.step_at(x1);
-        p_first = it.q.L - it.q.n + it.t0;
-        lo_all = first_key(p_first, w.window);
-        lo_last = first_key(it.hi - 1, w.window);
-        two = it.nt > w.tpt / 2;
-    }
-    // not every row sees every position of the step
-    __device__ __forceinline__ bool partial(const Item& it, int step) const {
-        const int k0 = it.lo + step * CH_KT;
+// What the roles need of an item, as the queue holds it.
+struct ChItem {
+    int s, hk, row0, nt;            // sequence, cache head, first row of q, tokens (-1: no more items)
+    int lo, hi, b0, b1;             // positions, and the steps of this CTA (b0 == b1: rows that see nothing)
+    int p_first, lo_all, lo_last;   // position of the first token, first positions of the first and the last token
+    int slot;                       // workspace slot of the part, -1: all steps are here
+    __device__ __forceinline__ bool partial(int step) const {      // not every row sees every position of the step
+        const int k0 = lo + step * CH_KT;
         return k0 < lo_last || k0 + CH_KT > p_first + 1;
     }
 };
+constexpr int CH_QUEUE = 4;
+constexpr int CH_READERS = 11;      // warps that read the queue: softmax, products, loads, V
 
 template <int NB>
 __global__ void __launch_bounds__(CH_THREADS, 1)
@@ -190,7 +198,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < B::N; ++i) {
             const bool warps = (i >= B::P && i < B::P + 2) || (i >= B::R && i < B::R + 2);    // one arrival per warp
-            mbar_init(&bars[i], warps ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : 1);
+            mbar_init(&bars[i], warps ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : i >= B::IE && i < B::IE + 4 ? CH_READERS : 1);
         }
         *abort_flag = 0;
         *odd_flag = 0;
@@ -214,6 +222,20 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int rows = w.tpt / 2 * w.gt;                    // query rows of a tile
     const int page = 1 << w.c.page_shift;
 
+    uint32_t n_it = 0;                                    // items this role has taken
+    ChItem im;
+    // the next item of the queue: false at the end, or if a role gave up
+    auto next_item = [&]() -> bool {
+        const uint32_t k = n_it % CH_QUEUE;
+        if (!__all_sync(0xffffffffu, wait_for(&bars[B::IF + k], n_it / CH_QUEUE & 1, abort_flag))) return false;
+        im = *reinterpret_cast<const ChItem*>(sm + SM::ITEMS + k * sizeof(ChItem));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B::IE + k]);
+        ++n_it;
+        return im.nt >= 0;
+    };
+    const int half = w.tpt / 2;                           // tokens of a tile
+
     if (!inside) {
         // nothing to do
     } else if (warp < 8) {
@@ -225,25 +247,28 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint32_t tS = taddr_of(tb, lanes, tile * 128), tO = taddr_of(tb, lanes, 256 + tile * 128);
         uint32_t nS = 0, nO = 0;
         bool ok = true;
-        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
-            if (it.steps == 0) {                          // every row sees nothing
-                const long long dst = it.a >= x0 && r < rows ? out_row(w, it, tile * rows + r, d) : -1;
+        while (ok && next_item()) {
+            const bool two = im.nt > half;
+            if (tile == 1 && !two) continue;
+            // row r of the tile: its token, its offset in the outputs (-1: none)
+            const int tok = tile * half + r / w.gt;
+            const long long dst = r < rows && tok < im.nt
+                                      ? ((long long)(im.row0 + tok) * (w.Hk * w.G) + im.hk * w.G + r % w.gt) * d : -1;
+            if (im.b0 == im.b1) {                         // every row sees nothing
                 if (dst >= 0)
                     for (int e = 0; e < d; e += 8) *reinterpret_cast<uint4*>(o + dst + e) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            const ChPart pt(w, it, x0, x1);
-            if (pt.b0 >= pt.b1 || (tile == 1 && !pt.two)) continue;
             // the tile's queries, eight 16-byte pieces of rows in flight per
             // thread; x / n = x * (65536 / n + 1) >> 16 for the small x and n here
             if (nO > 0) {                       // the last item's results have left the buffer
-                ok = __all_sync(0xffffffffu, wait_hot(&bars[B::R + tile], (nO - 1) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_for(&bars[B::R + tile], (nO - 1) & 1, abort_flag));
                 if (!ok) break;
             }
             {
-                const int per = d >> 3, t0 = tile * (w.tpt / 2);
+                const int per = d >> 3, t0 = tile * half;
                 const uint32_t mper = 65536 / per + 1, mgt = 65536 / w.gt + 1;
-                const __nv_bfloat16* qb = q + (it.q.r0 + it.t0 + t0) * q_stride + (long long)(it.hh * w.G) * d;
+                const __nv_bfloat16* qb = q + (im.row0 + t0) * q_stride + (long long)(im.hk * w.G) * d;
                 uint8_t* to = sm + SM::Q + tile * SM::TILE;
 #pragma unroll 1
                 for (int e0 = r; e0 < 128 * per; e0 += 128 * 8) {
@@ -251,10 +276,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const int e = e0 + u * 128, row = (int)(e * mper >> 16), ch = e - row * per;
-                        const int tok = (int)(row * mgt >> 16), g = row - tok * w.gt;
+                        const int tk = (int)(row * mgt >> 16), g = row - tk * w.gt;
                         v[u] = make_uint4(0, 0, 0, 0);
-                        if (row < rows && t0 + tok < it.nt)
-                            v[u] = *reinterpret_cast<const uint4*>(qb + tok * q_stride + g * d + ch * 8);
+                        if (row < rows && t0 + tk < im.nt)
+                            v[u] = *reinterpret_cast<const uint4*>(qb + tk * q_stride + g * d + ch * 8);
                     }
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
@@ -266,15 +291,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 fence_async_smem();
                 mbar_arrive(&bars[B::Q + tile]);
             }
-            const int tok = min(tile * (w.tpt / 2) + r / w.gt, it.nt - 1);
-            const int pos = pt.p_first + tok, lo = first_key(pos, w.window);
+            const int pos = im.p_first + min(tok, im.nt - 1), lo = first_key(pos, w.window);
             float m = -INFINITY, l = 0.f;
-            for (int step = pt.b0; step < pt.b1; ++step, ++nS) {
-                ok = __all_sync(0xffffffffu, wait_hot(&bars[B::S + tile], nS & 1, abort_flag));
+            for (int step = im.b0; step < im.b1; ++step, ++nS) {
+                ok = __all_sync(0xffffffffu, wait_for(&bars[B::S + tile], nS & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                if (pt.partial(it, step)) {              // masked scores become -inf in place
-                    const int k0 = it.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
+                if (im.partial(step)) {              // masked scores become -inf in place
+                    const int k0 = im.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 16) {
                         uint32_t v[16];
@@ -302,7 +326,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[124 + e]));
                 const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                if (step == pt.b0) {
+                if (step == im.b0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, (top - m) * scale2 > 8.f)) {
                     // S(step) is complete, so PV(step - 1), issued before it, is too
@@ -350,13 +374,12 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (lane == 0) mbar_arrive(&bars[B::P + tile]);
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait_hot(&bars[B::O + tile], nO & 1, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_for(&bars[B::O + tile], nO & 1, abort_flag));
             if (!ok) break;
             ++nO;
             tc_fence_after();
-            const bool whole = pt.b0 == 0 && pt.b1 == it.steps;
-            const long long dst = r < rows ? out_row(w, it, tile * rows + r, d) : -1;
-            const long long srow = (long long)(blockIdx.x * 2 + (it.a < x0 ? 0 : 1)) * sl.rows + tile * rows + r;
+            const bool whole = im.slot < 0;
+            const long long srow = (long long)im.slot * sl.rows + tile * rows + r;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             if (*odd_flag) {
                 // values that were cleaned out of V: a row gets the non-finite ones that it sees
@@ -365,14 +388,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     uint32_t v[16];
                     tmem_ld16(tO + c, v);
                     tmem_ld_wait();
-                    for (int step = pt.b0; step < pt.b1 && dst >= 0; ++step) {
-                        if (!pt.partial(it, step)) continue;
-                        const int k0 = it.lo + step * CH_KT;
+                    for (int step = im.b0; step < im.b1 && dst >= 0; ++step) {
+                        if (!im.partial(step)) continue;
+                        const int k0 = im.lo + step * CH_KT;
                         for (int j = max(k0, lo); j < min(k0 + CH_KT, pos + 1); ++j) {
-                            const int pg = load_page(w.c, it.s, j);
+                            const int pg = load_page(w.c, im.s, j);
                             if (pg < 0) continue;
                             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.c.v) + pg * w.c.page_stride +
-                                                       it.hh * w.c.head_stride + (j & (page - 1)) * w.c.row_stride + c;
+                                                       im.hk * w.c.head_stride + (j & (page - 1)) * w.c.row_stride + c;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const float x = __bfloat162float(src[e]);
@@ -450,7 +473,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         uint32_t slot = 0, ph = 0, fix = 0, phQ[2] = {0, 0}, phP[2] = {0, 0};
         bool ok = true;
         auto wait = [&](int bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, wait_hot(&bars[bar], parity, abort_flag));
+            ok = ok && __all_sync(0xffffffffu, wait_for(&bars[bar], parity, abort_flag));
             return ok;
         };
         auto advance = [&]() {
@@ -473,13 +496,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 mma_ts_if(one, tb + 256 + tile * 128, tb + tile * 128 + k * 8, b + (k * 2048 >> 4), id_o, !fresh || k > 0);
         };
         auto release = [&](uint32_t bar) { commit_if(one, &bars[bar]); };
-        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
-            const ChPart pt(w, it, x0, x1);
-            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+        while (ok && next_item()) {
+            if (im.b0 == im.b1) continue;
+            const bool two = im.nt > half;
             if (!wait(B::FULL + slot, ph)) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (i == 0 || pt.two) {
+                if (i == 0 || two) {
                     if (wait(B::Q + i, phQ[i])) {
                         phQ[i] ^= 1;
                         tc_fence_after();
@@ -489,11 +512,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (!ok) break;
             release(B::EMPTY + slot);
             advance();
-            for (int step = pt.b0; step < pt.b1 && ok; ++step) {
-                const bool more = step + 1 < pt.b1, fresh = step == pt.b0;
+            for (int step = im.b0; step < im.b1 && ok; ++step) {
+                const bool more = step + 1 < im.b1, fresh = step == im.b0;
                 const uint32_t vs = slot;
                 wait(B::FULL + vs, ph);
-                if (pt.partial(it, step)) {
+                if (im.partial(step)) {
                     wait(B::FIX + vs, fix >> vs & 1);
                     fix ^= 1u << vs;
                 }
@@ -501,13 +524,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (more) wait(B::FULL + slot, ph);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if ((i == 1 && !pt.two) || !wait(B::P + i, phP[i])) break;
+                    if ((i == 1 && !two) || !wait(B::P + i, phP[i])) break;
                     phP[i] ^= 1;
                     tc_fence_after();
                     issue_o(i, vs, fresh);
                     if (more) issue_s(i, slot);
                     else release(B::O + i);
-                    if (i == 1 || !pt.two) {
+                    if (i == 1 || !two) {
                         release(B::EMPTY + vs);
                         if (more) release(B::EMPTY + slot);
                     }
@@ -526,26 +549,25 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         uint32_t kv = 0;
         bool ok = true;
         const int box = min(page, CH_KT);
-        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
-            const ChPart pt(w, it, x0, x1);
-            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
+        while (ok && next_item()) {
+            if (im.b0 == im.b1) continue;
             // this lane's page of a step, or -1: no positions of the range in its box
             auto fetch = [&](int step) -> int {
-                const int k0 = it.lo + step * CH_KT, p = k0 + lane * box;
-                if (step >= pt.b1 || lane * box >= CH_KT || p >= it.hi || p + box <= pt.lo_all) return -1;
-                const int pg = load_page(w.c, it.s, p);
+                const int k0 = im.lo + step * CH_KT, p = k0 + lane * box;
+                if (step >= im.b1 || lane * box >= CH_KT || p >= im.hi || p + box <= im.lo_all) return -1;
+                const int pg = load_page(w.c, im.s, p);
                 return pg < 0 ? w.c.n_pages : pg;                 // a bad index: behind the pool, reads zeros
             };
-            int pg = fetch(pt.b0);
-            for (int step = pt.b0; step < pt.b1 && ok; ++step) {
+            int pg = fetch(im.b0);
+            for (int step = im.b0; step < im.b1 && ok; ++step) {
                 const int next = fetch(step + 1);
-                const int p = it.lo + step * CH_KT + lane * box;
+                const int p = im.lo + step * CH_KT + lane * box;
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box * 128 * NB;
                 for (int v = 0; v < 2; ++v, ++kv) {
                     const uint32_t slot = kv % ST;
                     uint64_t* bar = &bars[B::FULL + slot];
                     if (lane == 0) {
-                        if (kv >= ST) ok = wait_hot(&bars[B::EMPTY + slot], (kv / ST - 1) & 1, abort_flag);
+                        if (kv >= ST) ok = wait_for(&bars[B::EMPTY + slot], (kv / ST - 1) & 1, abort_flag);
                         if (ok) mbar_expect_tx(bar, bytes);
                     }
                     ok = __all_sync(0xffffffffu, ok);
@@ -554,7 +576,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (pg >= 0)
 #pragma unroll
                         for (int c = 0; c < NB; ++c)
-                            tma_load_4d(dst + c * 16384, v ? &tm_v : &tm_k, bar, c * 64, p & (page - 1), it.hh, pg);
+                            tma_load_4d(dst + c * 16384, v ? &tm_v : &tm_k, bar, c * 64, p & (page - 1), im.hk, pg);
                 }
                 pg = next;
             }
@@ -567,38 +589,39 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // ------------------------------------------------------------ V at the ends of the range
         uint32_t kv = 0;
         bool ok = true;
-        for (; it.s < w.b.nseq && it.a < x1 && ok; it.next(w)) {
-            const ChPart pt(w, it, x0, x1);
-            if (it.steps == 0 || pt.b0 >= pt.b1) continue;
-            for (int step = pt.b0; step < pt.b1 && ok; ++step, kv += 2) {
+        while (ok && next_item()) {
+            if (im.b0 == im.b1) continue;
+            for (int step = im.b0; step < im.b1 && ok; ++step, kv += 2) {
                 // every stage in its turn: a wait that skipped one could take an older phase for its own
                 const uint32_t vi = kv + 1, slot = vi % ST;
-                ok = wait_bar(&bars[B::FULL + kv % ST], (kv / ST) & 1, abort_flag) &&
-                     wait_bar(&bars[B::FULL + slot], (vi / ST) & 1, abort_flag);
+                ok = wait_for(&bars[B::FULL + kv % ST], (kv / ST) & 1, abort_flag) &&
+                     wait_for(&bars[B::FULL + slot], (vi / ST) & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (!pt.partial(it, step)) continue;
-                const int k0 = it.lo + step * CH_KT;
+                if (!im.partial(step)) continue;
+                const int k0 = im.lo + step * CH_KT;
                 uint8_t* V = sm + SM::KV + slot * SM::TILE;
-                bool odd = false;
-#pragma unroll 8
+                // rows outside the range to zero, the others looked at: a magnitude of 0x7f80 and up is not finite
+                uint32_t top = 0;
+#pragma unroll 4
                 for (int u = 0; u < NB * 32; ++u) {
                     const int row = (u % 32) * 4 + (lane >> 3);
                     uint4* at = reinterpret_cast<uint4*>(V + (u / 32) * 16384 + row * 128 + (lane & 7) * 16);
-                    const bool out = k0 + row < pt.lo_all || k0 + row >= it.hi;
-                    uint4 x = *at;
-                    const bool bad = nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
-                    if (out) {
+                    if (k0 + row < im.lo_all || k0 + row >= im.hi) {
                         *at = make_uint4(0, 0, 0, 0);
-                    } else if (bad) {
-                        odd = true;
-                        uint32_t* h = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((h[e] & 0x7f80u) == 0x7f80u) h[e] &= 0xffff0000u;
-                            if ((h[e] & 0x7f800000u) == 0x7f800000u) h[e] &= 0xffffu;
-                        }
-                        *at = x;
+                    } else {
+                        const uint4 x = *at;
+                        top = __vimax3_u16x2(top, x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);
+                        top = __vimax3_u16x2(top, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu);
+                    }
+                }
+                const bool odd = (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+                if (odd) {
+#pragma unroll 1
+                    for (int u = 0; u < NB * 32 * 8; ++u) {
+                        const int row = (u / 8 % 32) * 4 + (lane >> 3);
+                        uint16_t* at = reinterpret_cast<uint16_t*>(V + (u / 256) * 16384 + row * 128 + (lane & 7) * 16) + u % 8;
+                        if ((*at & 0x7fffu) >= 0x7f80u) *at = 0;
                     }
                 }
                 if (odd) *odd_flag = 1;
@@ -609,6 +632,28 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
         }
         if (!ok) *abort_flag = 1;
+    } else if (tid == CH_WALK) {
+        // ------------------------------------------------------------ the walk along the axis
+        bool ok = true, more = true;
+        while (more && ok) {
+            const uint32_t k = n_it % CH_QUEUE;
+            more = it.s < w.b.nseq && it.a < x1;
+            im.nt = -1;
+            if (more) {
+                const int b0 = it.step_at(x0), b1 = it.step_at(x1);
+                const bool mine = it.steps == 0 ? it.a >= x0 : b0 < b1;
+                im = ChItem{it.s, it.hh, it.ax.q.r0 + it.t0, it.nt, it.lo, it.hi, b0, b1, it.p_first,
+                            first_key(it.p_first, w.window), first_key(it.hi - 1, w.window),
+                            b0 == 0 && b1 == it.steps ? -1 : (int)blockIdx.x * 2 + (it.a < x0 ? 0 : 1)};
+                it.next(w);
+                if (!mine) continue;
+            }
+            if (n_it >= CH_QUEUE) ok = wait_for(&bars[B::IE + k], (n_it / CH_QUEUE - 1) & 1, abort_flag);
+            if (!ok) break;
+            *reinterpret_cast<ChItem*>(sm + SM::ITEMS + k * sizeof(ChItem)) = im;
+            mbar_arrive(&bars[B::IF + k]);
+            ++n_it;
+        }
     }
     }
     tc_fence_before();

@@ -101,7 +101,7 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
         if (b0 >= b1) continue;
         const int hk = it.hh / w.hs;
         const long long head_off = hk * w.c.head_stride;
-        const int p_first = it.q.L - it.q.n + it.t0;    // position of the tile's first token
+        const int p_first = it.p_first;
         const int lo_all = first_key(p_first, w.window);
         const int lo_last = first_key(it.hi - 1, w.window);       // the last token's first position
         auto page_of = [&](int step) -> int {           // -1 behind the part, or for a bad index
@@ -143,7 +143,7 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
                 const int r = g + 8 * half, tok = r / w.gt, hd = r - tok * w.gt;
                 const bool on = tok < it.nt && (it.hh % w.hs) * w.gt + hd < w.G;
                 prow[half] = p_first + min(tok, it.nt - 1);
-                const __nv_bfloat16* src = q + (it.q.r0 + it.t0 + tok) * q_stride + (long long)(h + hd) * d;
+                const __nv_bfloat16* src = q + (it.ax.q.r0 + it.t0 + tok) * q_stride + (long long)(h + hd) * d;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll

@@ -32,39 +32,48 @@ struct Work {
     int c0, min_chunk;
 };
 
-__device__ __forceinline__ long long tiles_cost(const Work& w, long long A, long long i) {
-    long long m = i;
-    if (w.window > 0) {
-        // first tile that the window cuts (A and the window are below 2^31)
-        const unsigned ahead = A < w.window - 1 ? (unsigned)(w.window - 1 - A) : 0u;
-        m = min(i, (long long)((ahead + w.tpt - 1) / w.tpt));
-    }
-    return m * (w.c0 + A) + w.tpt * (m * (m + 1) / 2) + (i - m) * ((long long)w.c0 + w.tpt + w.window - 1);
-}
+// one sequence on the axis
+struct SeqAxis {
+    Seq q;
+    int A, tiles, first;       // older positions, tiles, first tile that the window cuts (tiles: none)
 
-__device__ __forceinline__ int seq_tiles(const Work& w, const Seq& q) { return (q.n + w.tpt - 1) / w.tpt; }
-__device__ __forceinline__ long long seq_cost(const Work& w, const Seq& q) {
-    return tiles_cost(w, max(0, q.L - q.n), seq_tiles(w, q)) * (w.Hk * w.hs);
-}
+    __device__ __forceinline__ SeqAxis() {}
+    __device__ __forceinline__ SeqAxis(const Work& w, const Seq& seq) : q(seq) {
+        A = max(0, q.L - q.n);
+        tiles = (int)((unsigned)(q.n + w.tpt - 1) / (unsigned)w.tpt);
+        first = tiles;
+        if (w.window > 0) {
+            const unsigned ahead = A < w.window - 1 ? (unsigned)(w.window - 1 - A) : 0u;     // tokens it does not cut
+            first = min(tiles, (int)((ahead + w.tpt - 1) / (unsigned)w.tpt));
+        }
+    }
+    __device__ __forceinline__ long long upto(const Work& w, int i) const {       // cost of tiles 0 .. i-1
+        const long long m = min(i, first);
+        return m * (w.c0 + A) + w.tpt * (m * (m + 1) / 2) + (i - m) * ((long long)w.c0 + w.tpt + w.window - 1);
+    }
+    __device__ __forceinline__ long long tile(const Work& w, int i) const {       // cost of tile i
+        return i < first ? (long long)w.c0 + A + (long long)(i + 1) * w.tpt : (long long)w.c0 + w.tpt + w.window - 1;
+    }
+};
 
 // one item: its place on the axis and what it covers
 struct Item {
+    SeqAxis ax;
     int s, hh, i;              // sequence, head * hs + head part, tile
-    Seq q;
     long long a, cost;         // start and length on the axis
     int t0, nt;                // first token, tokens
+    int p_first;               // position of the first token
     int lo, hi;                // positions read (lo a multiple of the step), empty if hi <= 0
     int steps;
 
     __device__ __forceinline__ void fill(const Work& w) {
-        const long long A = max(0, q.L - q.n);
-        cost = tiles_cost(w, A, i + 1) - tiles_cost(w, A, i);
+        cost = ax.tile(w, i);
         t0 = i * w.tpt;
-        nt = min(w.tpt, q.n - t0);
-        const int p0 = q.L - q.n + t0;
-        lo = first_key(p0, w.window) & ~(w.kt - 1);
-        hi = p0 + nt;
-        steps = hi > lo ? (hi - lo + w.kt - 1) / w.kt : 0;
+        nt = min(w.tpt, ax.q.n - t0);
+        p_first = ax.q.L - ax.q.n + t0;
+        lo = first_key(p_first, w.window) & ~(w.kt - 1);
+        hi = p_first + nt;
+        steps = hi > lo ? (int)((unsigned)(hi - lo + w.kt - 1) / (unsigned)w.kt) : 0;
     }
     // first step at or behind place x of the axis. In float64: any monotone
     // function of x serves, as long as every caller computes the same.
@@ -75,14 +84,16 @@ struct Item {
     }
     __device__ __forceinline__ void next(const Work& w) {
         a += cost;
-        if (++i >= seq_tiles(w, q)) {
+        if (++i >= ax.tiles) {
             i = 0;
             if (++hh >= w.Hk * w.hs) {
                 hh = 0;
+                Seq q;
                 do {
                     if (++s >= w.b.nseq) return;
                     q = load_seq(w.b, w.c, s, false);
                 } while (q.n == 0);
+                ax = SeqAxis(w, q);
             }
         }
         fill(w);
@@ -102,9 +113,10 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
     const int per = (w.b.nseq + THREADS - 1) / THREADS;
     const int s0 = min(w.b.nseq, tid * per), s1 = min(w.b.nseq, s0 + per);
     long long sum = 0;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-        const Seq q = load_seq(w.b, w.c, s, true);
-        if (q.n > 0) sum += seq_cost(w, q);
+        const SeqAxis ax(w, load_seq(w.b, w.c, s, true));
+        sum += ax.upto(w, ax.tiles) * (w.Hk * w.hs);
     }
     long long inc = sum;
 #pragma unroll
@@ -121,28 +133,30 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
         if (i < warp) before += part[i];
         total += part[i];
     }
-    chunk = max((long long)w.min_chunk, (total + n_cta - 1) / n_cta);
+    chunk = (long long)((double)total / n_cta) + 1;           // n_cta chunks reach behind the end
+    chunk = max((long long)w.min_chunk, chunk);
     const long long x = chunk * index;
     if (x >= total) return false;
     if (x >= before && x < before + sum) {
+#pragma unroll 1
         for (int s = s0; s < s1; ++s) {
-            const Seq q = load_seq(w.b, w.c, s, false);
-            const long long cost = q.n > 0 ? seq_cost(w, q) : 0;
+            const SeqAxis ax(w, load_seq(w.b, w.c, s, false));
+            const long long per_head = ax.upto(w, ax.tiles), cost = per_head * (w.Hk * w.hs);
             if (x < before + cost) {
-                const long long A = max(0, q.L - q.n), per_head = tiles_cost(w, A, seq_tiles(w, q));
                 int hh = 0;
                 long long rem = x - before;
                 for (; rem >= per_head; ++hh) rem -= per_head;
-                int lo = 0, hi = seq_tiles(w, q) - 1;          // largest tile that starts at or before rem
+                int lo = 0, hi = ax.tiles - 1;                 // largest tile that starts at or before rem
+#pragma unroll 1
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (tiles_cost(w, A, mid) <= rem) lo = mid;
+                    if (ax.upto(w, mid) <= rem) lo = mid;
                     else hi = mid - 1;
                 }
                 found[0] = s;
                 found[1] = hh;
                 found[2] = lo;
-                found_a = before + hh * per_head + tiles_cost(w, A, lo);
+                found_a = before + hh * per_head + ax.upto(w, lo);
                 break;
             }
             before += cost;
@@ -153,7 +167,7 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
     item.hh = found[1];
     item.i = found[2];
     item.a = found_a;
-    item.q = load_seq(w.b, w.c, item.s, false);
+    item.ax = SeqAxis(w, load_seq(w.b, w.c, item.s, false));
     item.fill(w);
     return true;
 }
@@ -172,12 +186,15 @@ __device__ __forceinline__ long long out_row(const Work& w, const Item& it, int 
     const int part = it.hh % w.hs, h = it.hh / w.hs;
     const int head = part * w.gt + g;
     if (tok >= it.nt || head >= w.G) return -1;
-    return ((long long)(it.q.r0 + it.t0 + tok) * (w.Hk * w.G) + h * w.G + head) * d;
+    return ((long long)(it.ax.q.r0 + it.t0 + tok) * (w.Hk * w.G) + h * w.G + head) * d;
 }
 
 // Joins the parts of the items that were cut: block x of the grid looks at
 // the place where CTA x + 1 begins and takes the item there if the item's
-// first part is CTA x's. One warp per row.
+// first part is CTA x's. A warp takes rows one by one, a lane four columns;
+// the parts' weights are computed by lanes in parallel, 32 parts at a time,
+// and their rows added with sixteen loads in flight. Bound by latency and by
+// reading the parts once: a long decode's item has up to one part per CTA.
 constexpr int JOIN_WARPS = 8;
 
 template <typename T>
@@ -193,60 +210,71 @@ attn_join_kernel(Work w, Slots sl, T* __restrict__ o, int d, int n_cta) {
     if (!inside) return;
     const long long x = chunk * (first + 1);
     if (it.a == x || it.a < x - chunk) return;              // not cut here, or not here first
-    const int last = (int)((it.a + it.cost - 1) / chunk);
+    int last = (int)((double)(it.a + it.cost - 1) / (double)chunk);      // the CTA with the item's end, to within one
+    while (chunk * (last + 1) < it.a + it.cost) ++last;
+    while (chunk * last >= it.a + it.cost) --last;
+    // slots that hold a part (a CTA's interval may fall between two steps), in order
+    constexpr int MAX_PARTS = 1024;
+    __shared__ int part_slot[MAX_PARTS];
+    __shared__ int n_parts;
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int k0 = first; k0 <= last; k0 += 32) {
+            const int k = k0 + threadIdx.x;
+            const bool on = k <= last && it.step_at(chunk * k) < it.step_at(chunk * (k + 1));
+            const unsigned m = __ballot_sync(0xffffffffu, on);
+            if (on) part_slot[n + __popc(m & ((1u << threadIdx.x) - 1u))] = k * 2 + (k == first ? 1 : 0);
+            n += __popc(m);
+        }
+        if (threadIdx.x == 0) n_parts = n;
+    }
+    __syncthreads();
+    const int n = n_parts;
+    if (n <= 1) return;                  // one part holds all steps: its CTA wrote the rows
     const int lane = threadIdx.x & 31;
     const int rows = min(sl.rows, it.nt * w.gt);
+    const bool col = lane * 4 < d;
+#pragma unroll 1
     for (int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); r < rows; r += gridDim.y * JOIN_WARPS) {
         const long long dst = out_row(w, it, r, d);
         if (dst < 0) continue;
         float M = -INFINITY;
-        int parts = 0;
-        for (int k = first + lane; k <= last; k += 32) {
-            const int b = it.step_at(chunk * k), e = it.step_at(chunk * (k + 1));
-            if (b >= e) continue;
-            ++parts;
-            M = fmaxf(M, sl.ml[(k * 2 + (k == first ? 1 : 0)) * (long long)sl.rows + r].x);
-        }
+        for (int k = lane; k < n; k += 32) M = fmaxf(M, sl.ml[(long long)part_slot[k] * sl.rows + r].x);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-            parts += __shfl_xor_sync(0xffffffffu, parts, m);
-        }
-        if (parts <= 1) continue;            // one part holds all steps: its CTA wrote the row
+        for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
         const float base = M == -INFINITY ? 0.f : M;
         float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        for (int k0 = first; k0 <= last; k0 += 32) {
-            const int k = k0 + lane;
+#pragma unroll 1
+        for (int k0 = 0; k0 < n; k0 += 32) {
             float wt = 0.f;
-            bool on = false;
-            if (k <= last) {
-                on = it.step_at(chunk * k) < it.step_at(chunk * (k + 1));
-                if (on) {
-                    const float2 ml = sl.ml[(k * 2 + (k == first ? 1 : 0)) * (long long)sl.rows + r];
-                    wt = exp2f(ml.x - base);
-                    l += wt * ml.y;
-                }
+            if (k0 + lane < n) {
+                const float2 ml = sl.ml[(long long)part_slot[k0 + lane] * sl.rows + r];
+                wt = exp2f(ml.x - base);
+                l += wt * ml.y;
             }
-            const unsigned any = __ballot_sync(0xffffffffu, on);
-            const int cnt = min(32, last - k0 + 1);
-#pragma unroll 4
-            for (int j = 0; j < cnt; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, wt, j);
-                if (!(any >> j & 1u)) continue;
-                const float* src = sl.o + ((k0 + j) * 2 + (k0 + j == first ? 1 : 0)) * (long long)sl.rows * d +
-                                   (long long)r * d + lane * 4;
-                if (lane * 4 < d) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    acc[0] = fmaf(wj, v.x, acc[0]);
-                    acc[1] = fmaf(wj, v.y, acc[1]);
-                    acc[2] = fmaf(wj, v.z, acc[2]);
-                    acc[3] = fmaf(wj, v.w, acc[3]);
+#pragma unroll 1
+            for (int j = 0; j < min(32, n - k0); j += 16) {
+                float4 v[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (col && k0 + j + u < n)
+                        v[u] = *reinterpret_cast<const float4*>(sl.o + ((long long)part_slot[k0 + j + u] * sl.rows + r) * d +
+                                                                lane * 4);
+                }
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const float wu = __shfl_sync(0xffffffffu, wt, j + u);
+                    acc[0] = fmaf(wu, v[u].x, acc[0]);
+                    acc[1] = fmaf(wu, v[u].y, acc[1]);
+                    acc[2] = fmaf(wu, v[u].z, acc[2]);
+                    acc[3] = fmaf(wu, v[u].w, acc[3]);
                 }
             }
         }
         l = warp_sum(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (lane * 4 < d)
+        if (col)
 #pragma unroll
             for (int e = 0; e < 4; ++e) Elem<T>::st(o + dst + lane * 4 + e, acc[e] * inv);
     }
