@@ -68,17 +68,19 @@ jet_status launch_attn_simt(const void* q, int64_t q_stride, const attn::Cache& 
                   (long long)q_stride, c, b, (T*)o, Hq, Hk, d, window, scale);
 }
 
-// Workspace of a split attention launch: two slots per CTA.
+// Workspace of a split attention launch: two slots and a Cut per CTA.
 struct SlotLayout {
-    size_t ml, bytes;
+    size_t ml, cut, bytes;
 };
 SlotLayout slot_layout(int n_cta, int rows, int d) {
-    const size_t o = sizeof(float) * (size_t)n_cta * 2 * rows * d;
-    return SlotLayout{o, o + sizeof(float2) * (size_t)n_cta * 2 * rows};
+    const size_t o = sizeof(float) * (size_t)n_cta * 2 * rows * d, ml = sizeof(float2) * (size_t)n_cta * 2 * rows;
+    return SlotLayout{o, o + ml, o + ml + sizeof(attn::Cut) * (size_t)n_cta};
 }
 attn::Slots make_slots(void* ws, int n_cta, int rows, int d) {
     uint8_t* p = static_cast<uint8_t*>(ws);
-    return attn::Slots{reinterpret_cast<float*>(p), reinterpret_cast<float2*>(p + slot_layout(n_cta, rows, d).ml), rows};
+    const SlotLayout L = slot_layout(n_cta, rows, d);
+    return attn::Slots{reinterpret_cast<float*>(p), reinterpret_cast<float2*>(p + L.ml),
+                       reinterpret_cast<attn::Cut*>(p + L.cut), rows};
 }
 
 // tiles of `rows` query rows: whole tokens, or parts of one token's heads
@@ -88,11 +90,13 @@ attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, 
     return attn::Work{b, c, Hk, G, window, std::max(1, rows / G), gt, (G + gt - 1) / gt, kt, c0, min_chunk};
 }
 
+template <int RW, int SPLIT>
 jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
-    const int per = attn::JOIN_WARPS * 4;         // at most four rows to a warp
+    static_assert(3 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
+    const int per = attn::JOIN_WARPS / SPLIT * RW;
     const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
-    return launch(attn::attn_join_kernel<__nv_bfloat16>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, w, sl,
-                  (__nv_bfloat16*)o, d, n_cta);
+    return launch(attn::attn_join_kernel<__nv_bfloat16, RW, SPLIT>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
+                  (__nv_bfloat16*)o, w.Hk * w.G, d, w.gt);
 }
 
 template <int DP>
@@ -108,7 +112,7 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::DEC_THREADS), C::SMEM, s, (const __nv_bfloat16*)q,
                                  (long long)q_stride, w, sl, (__nv_bfloat16*)o, d, scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<1, 4>(w, sl, o, d, n_cta, s);
 }
 
 // pool [n_pages][Hk][page][d] as a 4-D tensor (d, page, Hk, n_pages): a box is 64 columns of up to 128 rows of one page
@@ -126,6 +130,19 @@ bool pool_map(CUtensorMap* m, const void* base, const attn::Cache& c, int Hk, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q [N][Hq][d] as a 3-D tensor (d, Hq, N): a box is 64 columns of the G heads of 128 / G tokens, the rows of one tile
+bool query_map(CUtensorMap* m, const void* q, int64_t q_stride, int N, int Hq, int G, int d) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hq, (cuuint64_t)N};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // query rows of an item: two tiles of whole tokens, at most 128 rows each
 int chunk_rows(int G) { return 2 * (128 / G) * G; }
 
@@ -137,18 +154,19 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
     attn::Work w = make_work(c, b, Hk, G, window, rows, attn::CH_KT, 256, 384);
     w.tpt = 2 * (128 / G);
     const attn::Slots sl = make_slots(ws, n_cta, rows, d);
-    CUtensorMap tk, tv;
-    if (!pool_map(&tk, c.k, c, Hk, d) || !pool_map(&tv, c.v, c, Hk, d)) return JET_ERR_CUDA;
+    CUtensorMap tk, tv, tq;
+    if (!pool_map(&tk, c.k, c, Hk, d) || !pool_map(&tv, c.v, c, Hk, d) || !query_map(&tq, q, q_stride, b.N, Hk * G, G, d))
+        return JET_ERR_CUDA;
     auto kern = attn::attn_chunk_kernel<NB>;
     if (smem_attr(kern, SM::BYTES) != JET_OK) return JET_ERR_CUDA;
-    const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv,
-                                 (const __nv_bfloat16*)q, (long long)q_stride, w, sl, (__nv_bfloat16*)o, d,
+    const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv, tq, w, sl,
+                                 (__nv_bfloat16*)o, d,
                                  scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<4, 1>(w, sl, o, d, n_cta, s);
 }
 
 // rows per sequence and cache head up to which the decode kernel is taken
-constexpr int kDecodeRows = 32;
+constexpr int kDecodeRows = 16;
 
 }  // namespace
 

@@ -16,11 +16,11 @@
 //                   maximum m is kept until a score exceeds it by 8 binades
 //                   (weights up to 2^8 are harmless in bf16 and float32), so O
 //                   is rescaled, by the same threads, only then. They also
-//                   load the item's queries and write its results.
+//                   write the item's results.
 //   warp 8          one lane issues all products
-//   warp 9          the TMA loads of K and V, one box per page (up to 128
-//                   rows) and lane, page indices a step ahead, through a ring of
-//                   32 KB stages that runs ahead into the next item
+//   warp 9          the TMA loads: the item's queries; K and V, one box per
+//                   page (up to 128 rows) and lane, page indices a step ahead,
+//                   through a ring of stages that runs ahead into the next item
 //   warp 10         cleans V at the ends of the range (below)
 //   warp 11         one lane walks the axis of the work and hands the items to
 //                   the other roles through a queue of four, so that the walk's
@@ -53,11 +53,12 @@ constexpr int CH_THREADS = 384, CH_KT = 128;
 constexpr int CH_MMA = 256, CH_LOAD = 288, CH_FIX = 320, CH_WALK = 352;       // first threads of warps 8 to 11
 
 template <int NB> struct ChSmem {                              // NB: 64-column blocks of d
-    static constexpr int STAGES = NB == 2 ? 5 : 8;
+    static constexpr int STAGES = NB == 2 ? 4 : 8;
     static constexpr uint32_t TILE = NB * 16384;
     static constexpr uint32_t Q = 0;                           // [2] tiles
     static constexpr uint32_t KV = Q + 2 * TILE;               // [STAGES] of K or V
-    static constexpr uint32_t BAR = KV + STAGES * TILE;
+    static constexpr uint32_t OUT = KV + STAGES * TILE;        // [8 warps] of 4 KB, results on their way out
+    static constexpr uint32_t BAR = OUT + 8 * 4096;
     static constexpr uint32_t MISC = BAR + 384;
     static constexpr uint32_t ITEMS = MISC + 64;               // [4] of the item queue
     static constexpr uint32_t BYTES = ITEMS + 4 * 48;
@@ -66,7 +67,7 @@ template <int NB> struct ChSmem {                              // NB: 64-column 
 
 template <int NB> struct ChBar {
     static constexpr int ST = ChSmem<NB>::STAGES;
-    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 2, R = O + 2, END = R + 2, IF = END + 1, IE = IF + 4, N = IE + 4;
+    static constexpr int FULL = 0, EMPTY = ST, FIX = 2 * ST, S = 3 * ST, P = S + 2, Q = P + 2, O = Q + 1, QE = O + 2, END = QE + 1, IF = END + 1, IE = IF + 4, N = IE + 4;
 };
 
 // D[tmem] (+)= A * B[smem], A in shared memory or in TMEM, where `one` holds.
@@ -180,7 +181,7 @@ constexpr int CH_READERS = 11;      // warps that read the queue: softmax, produ
 template <int NB>
 __global__ void __launch_bounds__(CH_THREADS, 1)
 attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __nv_bfloat16* __restrict__ q, long long q_stride, const Work w, const Slots sl,
+                  const __grid_constant__ CUtensorMap tm_q, const Work w, const Slots sl,
                   __nv_bfloat16* __restrict__ o, int d, float scale2) {
     typedef ChSmem<NB> SM;
     typedef ChBar<NB> B;
@@ -196,10 +197,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < B::N; ++i) {
-            const bool warps = (i >= B::P && i < B::P + 2) || (i >= B::R && i < B::R + 2);    // one arrival per warp
-            mbar_init(&bars[i], warps ? 4 : i >= B::Q && i < B::Q + 2 ? 128 : i >= B::IE && i < B::IE + 4 ? CH_READERS : 1);
-        }
+        for (int i = 0; i < B::N; ++i)
+            mbar_init(&bars[i], i >= B::P && i < B::P + 2 ? 4 : i >= B::IE && i < B::IE + 4 ? CH_READERS : 1);
         *abort_flag = 0;
         *odd_flag = 0;
         fence_mbar_init();
@@ -207,8 +206,18 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (tid == CH_LOAD) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_q);
     }
     if (warp == 0) tmem_alloc(tslot, 512);
+    {   // the rows of a query tile behind its last token's heads: never loaded, zero
+        const int idle = 128 - w.tpt / 2 * w.gt;
+        for (int e = tid; e < 2 * NB * idle * 8; e += CH_THREADS) {
+            const int blk = e / (idle * 8), rest = e - blk * idle * 8;
+            *reinterpret_cast<uint4*>(sm + SM::Q + blk * 16384 + (128 - idle + rest / 8) * 128 + (rest & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -237,7 +246,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int half = w.tpt / 2;                           // tokens of a tile
 
     if (!inside) {
-        // nothing to do
+        if (tid == 0) sl.cut[blockIdx.x] = Cut{0, 0, 0, 0, -1, 0, 0, 0};
     } else if (warp < 8) {
         // 256 x 200 + 128 x 96 registers of the 384 x 168 that the block starts with
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -259,62 +268,27 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     for (int e = 0; e < d; e += 8) *reinterpret_cast<uint4*>(o + dst + e) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            // the tile's queries, eight 16-byte pieces of rows in flight per
-            // thread; x / n = x * (65536 / n + 1) >> 16 for the small x and n here
-            if (nO > 0) {                       // the last item's results have left the buffer
-                ok = __all_sync(0xffffffffu, wait_for(&bars[B::R + tile], (nO - 1) & 1, abort_flag));
-                if (!ok) break;
-            }
-            {
-                const int per = d >> 3, t0 = tile * half;
-                const uint32_t mper = 65536 / per + 1, mgt = 65536 / w.gt + 1;
-                const __nv_bfloat16* qb = q + (im.row0 + t0) * q_stride + (long long)(im.hk * w.G) * d;
-                uint8_t* to = sm + SM::Q + tile * SM::TILE;
-#pragma unroll 1
-                for (int e0 = r; e0 < 128 * per; e0 += 128 * 8) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int e = e0 + u * 128, row = (int)(e * mper >> 16), ch = e - row * per;
-                        const int tk = (int)(row * mgt >> 16), g = row - tk * w.gt;
-                        v[u] = make_uint4(0, 0, 0, 0);
-                        if (row < rows && t0 + tk < im.nt)
-                            v[u] = *reinterpret_cast<const uint4*>(qb + tk * q_stride + g * d + ch * 8);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int e = e0 + u * 128, row = (int)(e * mper >> 16), ch = e - row * per;
-                        if (row < 128)
-                            *reinterpret_cast<uint4*>(to + (ch >> 3) * 16384 + sw128_off(row, (ch & 7) * 16)) = v[u];
-                    }
-                }
-                fence_async_smem();
-                mbar_arrive(&bars[B::Q + tile]);
-            }
             const int pos = im.p_first + min(tok, im.nt - 1), lo = first_key(pos, w.window);
             float m = -INFINITY, l = 0.f;
             for (int step = im.b0; step < im.b1; ++step, ++nS) {
                 ok = __all_sync(0xffffffffu, wait_for(&bars[B::S + tile], nS & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                if (im.partial(step)) {              // masked scores become -inf in place
-                    const int k0 = im.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 16) {
-                        uint32_t v[16];
-                        tmem_ld16(tS + c, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c + e > top || c + e < bot) v[e] = 0xff800000u;
-                        tmem_st16(tS + c, v);
-                    }
-                    tmem_st_wait();
-                }
                 uint32_t s[128];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) tmem_ld32(tS + u * 32, s + u * 32);
                 tmem_ld_wait();
+                if (im.partial(step)) {                  // columns outside bot .. top to -inf, by a bit mask of each 32
+                    const int k0 = im.lo + step * CH_KT, top = pos - k0, bot = lo - k0;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int a = min(32, max(0, bot - u * 32)), b = min(32, max(0, top + 1 - u * 32));
+                        const uint32_t seen = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(seen & (1u << c))) s[u * 32 + c] = 0xff800000u;
+                    }
+                }
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
@@ -408,9 +382,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     tmem_st_wait();
                 }
             }
-            // 32 columns at a time: rows to shared memory (the queries' buffer, free
-            // once O is complete), then out with consecutive lanes on a row
-            uint8_t* stage = sm + SM::Q + tile * SM::TILE + (warp & 3) * 4096;
+            // 32 columns at a time: rows to shared memory, then out with consecutive lanes on a row
+            uint8_t* stage = sm + SM::OUT + warp * 4096;
             const long long out = whole ? dst : dst < 0 ? -1 : srow * d;
 #pragma unroll 1
             for (int c = 0; c < d; c += 32) {
@@ -454,8 +427,6 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // the loads of O above are complete (waited for); the next item's products may
             // overwrite it once this thread has let them
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B::R + tile]);
         }
         if (!ok) *abort_flag = 1;
     } else {
@@ -470,7 +441,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int ks = d >> 4;
         const uint32_t one = elect_one();
         // ring position (stage, phase) of the next K or V, and the phases of the other barriers
-        uint32_t slot = 0, ph = 0, fix = 0, phQ[2] = {0, 0}, phP[2] = {0, 0};
+        uint32_t slot = 0, ph = 0, fix = 0, phQ = 0, phP[2] = {0, 0};
         bool ok = true;
         auto wait = [&](int bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, wait_for(&bars[bar], parity, abort_flag));
@@ -500,17 +471,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (im.b0 == im.b1) continue;
             const bool two = im.nt > half;
             if (!wait(B::FULL + slot, ph)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (i == 0 || two) {
-                    if (wait(B::Q + i, phQ[i])) {
-                        phQ[i] ^= 1;
-                        tc_fence_after();
-                        issue_s(i, slot);
-                    }
-                }
-            if (!ok) break;
+            if (!wait(B::Q, phQ)) break;
+            phQ ^= 1;
+            tc_fence_after();
+            issue_s(0, slot);
+            if (two) issue_s(1, slot);
             release(B::EMPTY + slot);
+            if (im.b0 + 1 == im.b1) release(B::QE);
             advance();
             for (int step = im.b0; step < im.b1 && ok; ++step) {
                 const bool more = step + 1 < im.b1, fresh = step == im.b0;
@@ -533,6 +500,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (i == 1 || !two) {
                         release(B::EMPTY + vs);
                         if (more) release(B::EMPTY + slot);
+                        if (step + 2 == im.b1) release(B::QE);      // the item's last scores: its queries are done
                     }
                 }
                 if (more) advance();
@@ -546,7 +514,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
     } else if (warp == CH_LOAD / 32) {
         // ------------------------------------------------------------ loads: lane e issues box e of a step
-        uint32_t kv = 0;
+        uint32_t kv = 0, nQ = 0;
         bool ok = true;
         const int box = min(page, CH_KT);
         while (ok && next_item()) {
@@ -559,6 +527,20 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 return pg < 0 ? w.c.n_pages : pg;                 // a bad index: behind the pool, reads zeros
             };
             int pg = fetch(im.b0);
+            // the item's queries, once the last item's scores are complete
+            if (lane == 0) {
+                if (nQ > 0) ok = wait_for(&bars[B::QE], (nQ - 1) & 1, abort_flag);
+                if (ok) {
+                    const bool two = im.nt > half;
+                    mbar_expect_tx(&bars[B::Q], (uint32_t)(two ? 2 : 1) * NB * rows * 128);
+                    for (int e = 0; e < (two ? 2 : 1) * NB; ++e)
+                        tma_load_3d(sm + SM::Q + e * 16384, &tm_q, &bars[B::Q], e % NB * 64, im.hk * w.G,
+                                    im.row0 + e / NB * half);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++nQ;
             for (int step = im.b0; step < im.b1 && ok; ++step) {
                 const int next = fetch(step + 1);
                 const int p = im.lo + step * CH_KT + lane * box;
@@ -583,6 +565,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         if (!ok) *abort_flag = 1;
         // every issued load has landed before the CTA frees its memory
+        if (lane == 0 && nQ > 0) mbar_wait(&bars[B::Q], (nQ - 1) & 1);
         if (lane == 0)
             for (uint32_t i = kv > ST ? kv - ST : 0; i < kv; ++i) mbar_wait(&bars[B::FULL + i % ST], (i / ST) & 1);
     } else if (tid >= CH_FIX && tid < CH_FIX + 32) {
@@ -601,16 +584,21 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (!im.partial(step)) continue;
                 const int k0 = im.lo + step * CH_KT;
                 uint8_t* V = sm + SM::KV + slot * SM::TILE;
-                // rows outside the range to zero, the others looked at: a magnitude of 0x7f80 and up is not finite
+                // rows outside the range to zero
+                const int ra = max(0, im.lo_all - k0), rb = min(CH_KT, im.hi - k0);
+#pragma unroll 1
+                for (int row = lane >> 3; row < CH_KT; row += 4)
+                    if (row < ra || row >= rb)
+#pragma unroll
+                        for (int c = 0; c < NB; ++c)
+                            *reinterpret_cast<uint4*>(V + c * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+                // then all looked at: a magnitude of 0x7f80 and up is not finite
                 uint32_t top = 0;
-#pragma unroll 4
-                for (int u = 0; u < NB * 32; ++u) {
-                    const int row = (u % 32) * 4 + (lane >> 3);
-                    uint4* at = reinterpret_cast<uint4*>(V + (u / 32) * 16384 + row * 128 + (lane & 7) * 16);
-                    if (k0 + row < im.lo_all || k0 + row >= im.hi) {
-                        *at = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint4 x = *at;
+                if (im.nt > 1) {
+#pragma unroll 8
+                    for (int u = 0; u < NB * 32; ++u) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(V + u * 512 + lane * 16);
                         top = __vimax3_u16x2(top, x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);
                         top = __vimax3_u16x2(top, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu);
                     }
@@ -619,8 +607,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (odd) {
 #pragma unroll 1
                     for (int u = 0; u < NB * 32 * 8; ++u) {
-                        const int row = (u / 8 % 32) * 4 + (lane >> 3);
-                        uint16_t* at = reinterpret_cast<uint16_t*>(V + (u / 256) * 16384 + row * 128 + (lane & 7) * 16) + u % 8;
+                        uint16_t* at = reinterpret_cast<uint16_t*>(V + (u >> 3) * 512 + lane * 16) + (u & 7);
                         if ((*at & 0x7fffu) >= 0x7f80u) *at = 0;
                     }
                 }
@@ -634,26 +621,30 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (!ok) *abort_flag = 1;
     } else if (tid == CH_WALK) {
         // ------------------------------------------------------------ the walk along the axis
+        Cut cut{0, 0, 0, 0, -1, 0, 0, 0};
         bool ok = true, more = true;
         while (more && ok) {
             const uint32_t k = n_it % CH_QUEUE;
             more = it.s < w.b.nseq && it.a < x1;
+            bool mine = true;
             im.nt = -1;
             if (more) {
                 const int b0 = it.step_at(x0), b1 = it.step_at(x1);
-                const bool mine = it.steps == 0 ? it.a >= x0 : b0 < b1;
+                mine = it.steps == 0 ? it.a >= x0 : b0 < b1;
                 im = ChItem{it.s, it.hh, it.ax.q.r0 + it.t0, it.nt, it.lo, it.hi, b0, b1, it.p_first,
                             first_key(it.p_first, w.window), first_key(it.hi - 1, w.window),
-                            b0 == 0 && b1 == it.steps ? -1 : (int)blockIdx.x * 2 + (it.a < x0 ? 0 : 1)};
-                it.next(w);
-                if (!mine) continue;
+                            note_item(w, it, blockIdx.x, x0, x1, chunk, b0, b1, cut)};
             }
-            if (n_it >= CH_QUEUE) ok = wait_for(&bars[B::IE + k], (n_it / CH_QUEUE - 1) & 1, abort_flag);
-            if (!ok) break;
-            *reinterpret_cast<ChItem*>(sm + SM::ITEMS + k * sizeof(ChItem)) = im;
-            mbar_arrive(&bars[B::IF + k]);
-            ++n_it;
+            if (mine) {
+                if (n_it >= CH_QUEUE) ok = wait_for(&bars[B::IE + k], (n_it / CH_QUEUE - 1) & 1, abort_flag);
+                if (!ok) break;
+                *reinterpret_cast<ChItem*>(sm + SM::ITEMS + k * sizeof(ChItem)) = im;
+                mbar_arrive(&bars[B::IF + k]);
+                ++n_it;
+            }
+            if (more) it.next(w);
         }
+        sl.cut[blockIdx.x] = cut;
     }
     }
     tc_fence_before();

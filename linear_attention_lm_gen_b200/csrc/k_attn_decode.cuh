@@ -81,7 +81,11 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
     pdl_trigger();
     long long chunk, total;
     Item it;
-    if (!block_locate<DEC_THREADS>(w, gridDim.x, blockIdx.x, chunk, total, it)) return;
+    Cut cut{0, 0, 0, 0, -1, 0, 0, 0};
+    if (!block_locate<DEC_THREADS>(w, gridDim.x, blockIdx.x, chunk, total, it)) {
+        if (tid == 0) sl.cut[blockIdx.x] = cut;
+        return;
+    }
     const long long x0 = chunk * blockIdx.x, x1 = min(total, x0 + chunk);
     const unsigned char* kp = static_cast<const unsigned char*>(w.c.k);
     const unsigned char* vp = static_cast<const unsigned char*>(w.c.v);
@@ -89,6 +93,7 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
 
     for (; it.s < w.b.nseq && it.a < x1; it.next(w)) {
         const int b0 = it.step_at(x0), b1 = it.step_at(x1);
+        const int slot = note_item(w, it, blockIdx.x, x0, x1, chunk, b0, b1, cut);
         if (it.steps == 0) {                            // every row sees nothing: the CTA with the item's start
             if (it.a >= x0)
                 for (int r = warp; r < DEC_ROWS; r += DEC_WARPS) {
@@ -288,8 +293,7 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
         }
         __syncthreads();
         {
-            const bool whole = b0 == 0 && b1 == it.steps;
-            const int slot = blockIdx.x * 2 + (it.a < x0 ? 0 : 1);
+            const bool whole = slot < 0;
             const int r = tid / 8, c8 = tid % 8;                    // 16 rows, 8 lanes each
             const long long dst = out_row(w, it, r, d);
             if (dst >= 0) {
@@ -328,6 +332,7 @@ attn_decode_kernel(const __nv_bfloat16* __restrict__ q, long long q_stride, Work
         }
         __syncthreads();
     }
+    if (tid == 0) sl.cut[blockIdx.x] = cut;
 }
 
 }  // namespace attn

@@ -172,13 +172,46 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
     return true;
 }
 
+// What a CTA leaves for the join: the item that starts in its interval and is
+// cut at its end, if there is one, and which of its slots it filled.
+struct Cut {
+    int row0, nt;              // first row of q and tokens of that item
+    int head0, heads;          // first query head and heads
+    int last;                  // the CTA with the item's end; -1: no such item
+    int has0, has1;
+    int pad;
+};
+
 // Workspace: per CTA two slots, each `rows` rows of d float32 sums and the
-// rows' (maximum, sum) pairs, in units of base-2 logits.
+// rows' (maximum, sum) pairs, in units of base-2 logits, and a Cut.
 struct Slots {
     float* o;          // [n_cta * 2][rows][d]
     float2* ml;        // [n_cta * 2][rows]
+    Cut* cut;          // [n_cta]
     int rows;
 };
+
+// Enter an item of CTA `me` (interval x0 .. x1, its steps b0 .. b1) into the
+// CTA's Cut; the slot its part goes to, or -1 if all steps are here.
+__device__ __forceinline__ int note_item(const Work& w, const Item& it, int me, long long x0, long long x1, long long chunk,
+                                         int b0, int b1, Cut& cut) {
+    const bool part = b0 < b1 && !(b0 == 0 && b1 == it.steps);
+    const bool older = it.a < x0;
+    if (older && part) cut.has0 = 1;
+    if (!older && it.a + it.cost > x1) {
+        const long long end = it.a + it.cost - 1;
+        int last = (int)((double)end / (double)chunk);          // to within one
+        if (chunk * (last + 1) <= end) ++last;
+        if (chunk * last > end) --last;
+        cut.row0 = it.ax.q.r0 + it.t0;
+        cut.nt = it.nt;
+        cut.head0 = it.hh / w.hs * w.G + it.hh % w.hs * w.gt;
+        cut.heads = min(w.gt, w.G - it.hh % w.hs * w.gt);
+        cut.last = last;
+        cut.has1 = part;
+    }
+    return part ? me * 2 + (older ? 0 : 1) : -1;
+}
 
 // element offset of row r of an item in the packed [N, Hq, d] outputs, or -1
 __device__ __forceinline__ long long out_row(const Work& w, const Item& it, int r, int d) {
@@ -189,39 +222,38 @@ __device__ __forceinline__ long long out_row(const Work& w, const Item& it, int 
     return ((long long)(it.ax.q.r0 + it.t0 + tok) * (w.Hk * w.G) + h * w.G + head) * d;
 }
 
-// Joins the parts of the items that were cut: block x of the grid looks at
-// the place where CTA x + 1 begins and takes the item there if the item's
-// first part is CTA x's. A warp takes rows one by one, a lane four columns;
+// Joins the parts of the items that were cut, in the order of the CTAs: block
+// x of the grid takes the item that was cut at the end of CTA x's interval, if
+// it started there. A warp takes RW rows at once, a lane four columns of each;
 // the parts' weights are computed by lanes in parallel, 32 parts at a time,
-// and their rows added with sixteen loads in flight. Bound by latency and by
-// reading the parts once: a long decode's item has up to one part per CTA.
+// and their rows added with sixteen loads in flight. SPLIT warps share the
+// parts of a row (a long decode's item has a part in every CTA: bound by the
+// latency of its batches of loads) and meet in shared memory.
 constexpr int JOIN_WARPS = 8;
+constexpr int MAX_PARTS = 1024;
 
-template <typename T>
-__global__ void __launch_bounds__(JOIN_WARPS * 32)
-attn_join_kernel(Work w, Slots sl, T* __restrict__ o, int d, int n_cta) {
-    // cu_q and kv_lens are final before the kernel ahead of this one began
-    long long chunk, total;
-    Item it;
-    const int first = blockIdx.x;
-    const bool inside = block_locate<JOIN_WARPS * 32>(w, n_cta, first + 1, chunk, total, it);
-    pdl_wait();        // in every block: the next kernel's wait covers the parts' kernel through this one
-    pdl_trigger();
-    if (!inside) return;
-    const long long x = chunk * (first + 1);
-    if (it.a == x || it.a < x - chunk) return;              // not cut here, or not here first
-    int last = (int)((double)(it.a + it.cost - 1) / (double)chunk);      // the CTA with the item's end, to within one
-    while (chunk * (last + 1) < it.a + it.cost) ++last;
-    while (chunk * last >= it.a + it.cost) --last;
-    // slots that hold a part (a CTA's interval may fall between two steps), in order
-    constexpr int MAX_PARTS = 1024;
-    __shared__ int part_slot[MAX_PARTS];
+template <typename T, int RW, int SPLIT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 2)
+attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
+    static_assert(SPLIT == 1 || RW == 1, "one row to a group of warps");
+    constexpr int PB = 16 / RW;                             // parts of a batch of loads
+    constexpr int ROWS = JOIN_WARPS / SPLIT * RW;           // rows of a block
+    __shared__ int part_slot[MAX_PARTS + PB];
     __shared__ int n_parts;
+    __shared__ float4 meet[SPLIT > 1 ? JOIN_WARPS : 1][32];
+    __shared__ float meet_l[JOIN_WARPS];
+    pdl_wait();
+    pdl_trigger();
+    const int first = blockIdx.x;
+    const Cut me = sl.cut[first];
+    if (me.last <= first) return;
+    const int rows = me.nt * gt;
+    if ((int)blockIdx.y * ROWS >= rows) return;
     if (threadIdx.x < 32) {
         int n = 0;
-        for (int k0 = first; k0 <= last; k0 += 32) {
+        for (int k0 = first; k0 <= me.last; k0 += 32) {
             const int k = k0 + threadIdx.x;
-            const bool on = k <= last && it.step_at(chunk * k) < it.step_at(chunk * (k + 1));
+            const bool on = k <= me.last && (k == first ? me.has1 : sl.cut[min(k, me.last)].has0);
             const unsigned m = __ballot_sync(0xffffffffu, on);
             if (on) part_slot[n + __popc(m & ((1u << threadIdx.x) - 1u))] = k * 2 + (k == first ? 1 : 0);
             n += __popc(m);
@@ -230,53 +262,91 @@ attn_join_kernel(Work w, Slots sl, T* __restrict__ o, int d, int n_cta) {
     }
     __syncthreads();
     const int n = n_parts;
-    if (n <= 1) return;                  // one part holds all steps: its CTA wrote the rows
-    const int lane = threadIdx.x & 31;
-    const int rows = min(sl.rows, it.nt * w.gt);
+    if (n == 0) return;                  // one CTA had all steps after all, and wrote the rows
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r0 = blockIdx.y * ROWS + warp / SPLIT * RW, share = warp % SPLIT;
     const bool col = lane * 4 < d;
-#pragma unroll 1
-    for (int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); r < rows; r += gridDim.y * JOIN_WARPS) {
-        const long long dst = out_row(w, it, r, d);
-        if (dst < 0) continue;
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32) M = fmaxf(M, sl.ml[(long long)part_slot[k] * sl.rows + r].x);
+    const int rmax = min(rows, sl.rows) - 1;
+    float M[RW], l[RW], acc[RW][4];
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-        const float base = M == -INFINITY ? 0.f : M;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 1
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            float wt = 0.f;
-            if (k0 + lane < n) {
-                const float2 ml = sl.ml[(long long)part_slot[k0 + lane] * sl.rows + r];
-                wt = exp2f(ml.x - base);
-                l += wt * ml.y;
-            }
-#pragma unroll 1
-            for (int j = 0; j < min(32, n - k0); j += 16) {
-                float4 v[16];
+    for (int u = 0; u < RW; ++u) {
+        M[u] = -INFINITY;
+        l[u] = 0.f;
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (col && k0 + j + u < n)
-                        v[u] = *reinterpret_cast<const float4*>(sl.o + ((long long)part_slot[k0 + j + u] * sl.rows + r) * d +
-                                                                lane * 4);
-                }
+        for (int e = 0; e < 4; ++e) acc[u][e] = 0.f;
+    }
+    for (int k = lane; k < n; k += 32) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    const float wu = __shfl_sync(0xffffffffu, wt, j + u);
-                    acc[0] = fmaf(wu, v[u].x, acc[0]);
-                    acc[1] = fmaf(wu, v[u].y, acc[1]);
-                    acc[2] = fmaf(wu, v[u].z, acc[2]);
-                    acc[3] = fmaf(wu, v[u].w, acc[3]);
-                }
+        for (int u = 0; u < RW; ++u) M[u] = fmaxf(M[u], sl.ml[(long long)part_slot[k] * sl.rows + min(r0 + u, rmax)].x);
+    }
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) M[u] = fmaxf(M[u], __shfl_xor_sync(0xffffffffu, M[u], m));
+        if (M[u] == -INFINITY) M[u] = 0.f;
+    }
+    const int k_begin = n * share / SPLIT, k_end = n * (share + 1) / SPLIT;
+#pragma unroll 1
+    for (int k0 = k_begin; k0 < k_end; k0 += 32) {
+        float wt[RW];
+#pragma unroll
+        for (int u = 0; u < RW; ++u) {
+            wt[u] = 0.f;
+            if (k0 + lane < k_end) {
+                const float2 ml = sl.ml[(long long)part_slot[k0 + lane] * sl.rows + min(r0 + u, rmax)];
+                wt[u] = exp2f(ml.x - M[u]);
+                l[u] += wt[u] * ml.y;
             }
         }
-        l = warp_sum(l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (col)
+#pragma unroll 1
+        for (int j = 0; j < min(32, k_end - k0); j += PB) {
+            float4 v[PB][RW];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) Elem<T>::st(o + dst + lane * 4 + e, acc[e] * inv);
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int u = 0; u < RW; ++u) {
+                    v[p][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (col && k0 + j + p < k_end)
+                        v[p][u] = *reinterpret_cast<const float4*>(
+                            sl.o + ((long long)part_slot[k0 + j + p] * sl.rows + min(r0 + u, rmax)) * d + lane * 4);
+                }
+#pragma unroll
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int u = 0; u < RW; ++u) {
+                    const float x = __shfl_sync(0xffffffffu, wt[u], j + p);
+                    acc[u][0] = fmaf(x, v[p][u].x, acc[u][0]);
+                    acc[u][1] = fmaf(x, v[p][u].y, acc[u][1]);
+                    acc[u][2] = fmaf(x, v[p][u].z, acc[u][2]);
+                    acc[u][3] = fmaf(x, v[p][u].w, acc[u][3]);
+                }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < RW; ++u) l[u] = warp_sum(l[u]);
+    if (SPLIT > 1) {
+        meet[warp][lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        if (lane == 0) meet_l[warp] = l[0];
+        __syncthreads();
+        if (share > 0) return;
+#pragma unroll
+        for (int p = 1; p < SPLIT; ++p) {
+            const float4 v = meet[warp + p][lane];
+            acc[0][0] += v.x;
+            acc[0][1] += v.y;
+            acc[0][2] += v.z;
+            acc[0][3] += v.w;
+            l[0] += meet_l[warp + p];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+        const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
+        const int r = r0 + u, tok = r / gt, g = r - tok * gt;
+        if (r >= rows || g >= me.heads || !col) continue;
+        T* dst = o + ((long long)(me.row0 + tok) * Hq + me.head0 + g) * d + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Elem<T>::st(dst + e, acc[u][e] * inv);
     }
 }
 
