@@ -504,83 +504,110 @@ def jet_conv_gdn_decode_step(q, k, v, hist_in, hist_out, taps, g, beta, S, o=Non
 
 
 # ---------------------------------------------------------------- softmax attention over a paged cache
+# The decode step's calls take a few microseconds on the GPU, so their checks
+# are written to cost little: one expression per argument, the error worked out
+# only when it fails.
 class _on:
-    """Make `device` current and issue on `stream` (default: the device's
+    """Make device `index` current and issue on `stream` (default: the device's
     current stream) for the length of a call; what the call allocates belongs
-    to that stream. Every tensor of the call has to be on `device`."""
+    to that stream. Every tensor of the call has to be on the device."""
 
-    def __init__(self, device, stream):
-        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self._stream, self._ctx = stream, None
+    __slots__ = ("_dev", "_stream", "_index")
+
+    def __init__(self, index, stream):
+        self._index, self._stream, self._dev = index, stream, None
 
     def __enter__(self):
-        if self._dev is not None:
+        index, stream = self._index, self._stream
+        if index != torch._C._cuda_getDevice():
+            self._dev = torch.cuda.device(index)
             self._dev.__enter__()
-        if self._stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        raw = self._stream.cuda_stream if hasattr(self._stream, "cuda_stream") else int(self._stream)
-        if raw:
-            self._ctx = torch.cuda.stream(torch.cuda.ExternalStream(raw))
-            self._ctx.__enter__()
-        return ctypes.c_void_p(raw)
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(index)
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        self._stream = torch.cuda.stream(torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream(index))
+        self._stream.__enter__()
+        return raw
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
         if self._dev is not None:
             self._dev.__exit__(*exc)
         return False
 
 
-def _ptr_on(t, name, device, dtype=None, shape=None):
-    if t is None:
-        return None
-    p = _ptr(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return p
-
-
-def _rows(t, name, dtype, shape, device):
-    """[N, heads, d] with dense rows of heads: (address, elements between tokens)."""
+def _refuse(t, name, index, dtype, shape):
+    """Raise what is wrong with an argument that has to be a tensor of this dtype and shape on GPU `index`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} has strides {t.stride()}: it must be contiguous, its last axis and its heads dense")
+
+
+def _index(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _dense(t, name, index, dtype, shape):
+    """Address of a contiguous tensor of this dtype and shape on GPU `index`."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(t, name, index, dtype, shape)
+    return t.data_ptr()
+
+
+def _scratch(t, name, index):
+    """Address and bytes of a workspace."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous()):
+        _refuse(t, name, index, None, None)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _rows(t, name, index, dtype, shape):
+    """[N, heads, d] with dense rows of heads: (address, elements between tokens)."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape):
+        _refuse(t, name, index, dtype, shape)
     N, H, d = shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-        raise ValueError(f"{name} must have dense heads (strides {t.stride()})")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if N > 1 else H * d)
+    sn, sh, sd = t.stride()
+    if sd != 1 or (sh != d and H > 1):
+        _refuse(t, name, index, dtype, shape)
+    return t.data_ptr(), (sn if N > 1 else H * d)
 
 
-def _kv_pools(k_pool, v_pool, dtype, Hk, d, device):
-    """The pools' addresses and their common strides (page, head, row)."""
+def _kv_pools(k_pool, v_pool, index, dtype, Hk, d):
+    """The pools' addresses, their common strides (page, head, row), pages and page size."""
     for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != 4 or t.shape[1] != Hk or t.shape[3] != d or t.shape != k_pool.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, {Hk}, page, {d}]")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.stride(3) != 1 or t.stride() != k_pool.stride():
-            raise ValueError("k_pool and v_pool must have the same strides and dense rows")
-    st = [k_pool.stride(i) if k_pool.shape[i] > 1 else d for i in range(3)]
-    return ctypes.c_void_p(k_pool.data_ptr()), ctypes.c_void_p(v_pool.data_ptr()), st
+        if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.dim() == 4):
+            _refuse(t, name, index, dtype, None if isinstance(t, torch.Tensor) and t.dim() == 4 else ("pages", Hk, "page", d))
+    shape, st = k_pool.shape, k_pool.stride()
+    if shape[1] != Hk or shape[3] != d or v_pool.shape != shape:
+        raise ValueError(f"the pools have shapes {tuple(shape)} and {tuple(v_pool.shape)}, expected [pages, {Hk}, page, {d}]")
+    if st[3] != 1 or v_pool.stride() != st:
+        raise ValueError("k_pool and v_pool must have the same strides and dense rows")
+    if 1 in shape:                           # an axis of one entry has no stride that matters
+        st = [st[i] if shape[i] > 1 else d for i in range(3)]
+    return k_pool.data_ptr(), v_pool.data_ptr(), st[0], st[1], st[2], shape[0], shape[2]
 
 
-def _batch(cu_q, kv_lens, page_table, device):
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be [nseq, max_pages]")
+_I32 = torch.int32
+
+
+def _batch(cu_q, kv_lens, page_table, index):
+    if not (isinstance(page_table, torch.Tensor) and page_table.get_device() == index and page_table.dtype is _I32
+            and page_table.dim() == 2 and page_table.is_contiguous()):
+        _refuse(page_table, "page_table", index, _I32, None if isinstance(page_table, torch.Tensor)
+                and page_table.dim() == 2 else ("nseq", "max_pages"))
     nseq, max_pages = page_table.shape
-    return (_ptr_on(cu_q, "cu_q", device, torch.int32, (nseq + 1,)),
-            _ptr_on(kv_lens, "kv_lens", device, torch.int32, (nseq,)),
-            _ptr_on(page_table, "page_table", device, torch.int32), nseq, max_pages)
+    return (_dense(cu_q, "cu_q", index, _I32, (nseq + 1,)), _dense(kv_lens, "kv_lens", index, _I32, (nseq,)),
+            page_table.data_ptr(), nseq, max_pages)
 
 
 def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, page_table, k_pool, v_pool, q_out=None, *,
@@ -592,29 +619,33 @@ def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, pag
     projection's output. cu_q [nseq+1], kv_lens [nseq] (new tokens included)
     and page_table [nseq,max_pages] are int32 on the GPU. q_out may be q
     itself. Returns q_out [N,Hq,d]."""
-    L = load_library()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    N, Hq, d = q.shape
-    Hk, dev, dt = k.shape[1], q.device, q.dtype
-    code = _dt(q)
-    qp, qs = _rows(q, "q", dt, (N, Hq, d), dev)
-    kp, ks = _rows(k, "k", dt, (N, Hk, d), dev)
-    vp, vs = _rows(v, "v", dt, (N, Hk, d), dev)
-    kpool, vpool, pst = _kv_pools(k_pool, v_pool, dt, Hk, d, dev)
-    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, dev)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    gq = _ptr_on(q_gamma, "q_gamma", dev, torch.float32, (d,))
-    gk = _ptr_on(k_gamma, "k_gamma", dev, torch.float32, (d,))
-    fr = _ptr_on(inv_freq, "inv_freq", dev, torch.float32)
-    with _on(dev, stream) as s:
+    L = _lib or load_library()
+    index = _index(q, "q")
+    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q, k and v must be [N, heads, d]")
+    dt, shape = q.dtype, q.shape
+    N, Hq, d = shape
+    Hk = k.shape[1]
+    code, kv_shape = _dt(q), (N, Hk, d)
+    qp, qs = _rows(q, "q", index, dt, shape)
+    kp, ks = _rows(k, "k", index, dt, kv_shape)
+    vp, vs = _rows(v, "v", index, dt, kv_shape)
+    kpool, vpool, ps, hs, rs, n_pages, page = _kv_pools(k_pool, v_pool, index, dt, Hk, d)
+    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, index)
+    gq = None if q_gamma is None else _dense(q_gamma, "q_gamma", index, torch.float32, (d,))
+    gk = None if k_gamma is None else _dense(k_gamma, "k_gamma", index, torch.float32, (d,))
+    rot, fr = 0, None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        fr = _dense(inv_freq, "inv_freq", index, torch.float32, (rot // 2,))
+    with _on(index, stream) as s:
         if q_out is None:
-            q_out = torch.empty((N, Hq, d), device=dev, dtype=dt)
-        op, os_ = _rows(q_out, "q_out", dt, (N, Hq, d), dev)
-        st = L.jet_attn_rope_append(qp, qs, kp, ks, vp, vs, gq, gk, float(eps), fr, rot, int(bool(interleaved)), op,
-                                    os_, kpool, vpool, *pst, cu, kl, pt, nseq, N, max_pages, k_pool.shape[0],
-                                    k_pool.shape[2], Hq, Hk, d, code, s)
-    _check("jet_attn_rope_append", st)
+            q_out = torch.empty((N, Hq, d), device=q.device, dtype=dt)
+        op, os_ = _rows(q_out, "q_out", index, dt, shape)
+        st = L.jet_attn_rope_append(qp, qs, kp, ks, vp, vs, gq, gk, eps, fr, rot, 1 if interleaved else 0, op, os_, kpool,
+                                    vpool, ps, hs, rs, cu, kl, pt, nseq, N, max_pages, n_pages, page, Hq, Hk, d, code, s)
+    if st:
+        raise JetError("jet_attn_rope_append", st)
     return q_out
 
 
@@ -632,29 +663,28 @@ def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 
     token sees, its own included (0: all). scale: 1/sqrt(d) by default.
     max_new: the largest number of new tokens of a sequence (0: unknown); it
     only chooses the kernel. Returns o [N,Hq,d]."""
-    L = load_library()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    N, Hq, d = q.shape
-    dev, dt = q.device, q.dtype
-    code = _dt(q)
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
-        raise ValueError("k_pool must be [pages, Hk, page, d]")
-    Hk = k_pool.shape[1]
-    qp, qs = _rows(q, "q", dt, (N, Hq, d), dev)
-    kpool, vpool, pst = _kv_pools(k_pool, v_pool, dt, Hk, d, dev)
-    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, dev)
-    with _on(dev, stream) as s:
+    L = _lib or load_library()
+    index = _index(q, "q")
+    if q.dim() != 3 or not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("q must be [N, Hq, d] and the pools [pages, Hk, page, d]")
+    dt, shape = q.dtype, q.shape
+    N, Hq, d = shape
+    code, Hk = _dt(q), k_pool.shape[1]
+    qp, qs = _rows(q, "q", index, dt, shape)
+    kpool, vpool, ps, hs, rs, n_pages, page = _kv_pools(k_pool, v_pool, index, dt, Hk, d)
+    cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, index)
+    with _on(index, stream) as s:
         if o is None:
-            o = torch.empty((N, Hq, d), device=dev, dtype=dt)
+            o = torch.empty((N, Hq, d), device=q.device, dtype=dt)
         if workspace is None:
-            workspace = torch.empty(max(16, L.jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, code)), device=dev,
+            workspace = torch.empty(max(16, L.jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, code)), device=q.device,
                                     dtype=torch.uint8)
-        st = L.jet_attn_paged(qp, qs, kpool, vpool, *pst, cu, kl, pt, _ptr_on(o, "o", dev, dt, (N, Hq, d)),
-                              _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size(), nseq,
-                              N, int(max_new), max_pages, k_pool.shape[0], k_pool.shape[2], Hq, Hk, d, int(window),
-                              float(d ** -0.5 if scale is None else scale), code, s)
-    _check("jet_attn_paged", st)
+        wp, wn = _scratch(workspace, "workspace", index)
+        st = L.jet_attn_paged(qp, qs, kpool, vpool, ps, hs, rs, cu, kl, pt, _dense(o, "o", index, dt, shape), wp, wn,
+                              nseq, N, max_new, max_pages, n_pages, page, Hq, Hk, d, window,
+                              d ** -0.5 if scale is None else scale, code, s)
+    if st:
+        raise JetError("jet_attn_paged", st)
     return o
 
 
@@ -664,33 +694,30 @@ def _entries(pools, what="pools"):
     same number of entries along their first axis, each entry dense."""
     if isinstance(pools, torch.Tensor) or len(pools) == 0:
         raise TypeError(f"{what} must be a non-empty list of tensors")
-    first = pools[0]
-    n = len(pools)
-    base, size, step = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int64 * n)()
-    for i, t in enumerate(pools):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{what}[{i}] must be a CUDA tensor")
-        if t.device != first.device:
-            raise ValueError(f"{what}[{i}] is on {t.device}, expected {first.device}")
-        if t.dim() < 2 or t.shape[0] != first.shape[0]:
-            raise ValueError(f"{what}[{i}] has shape {tuple(t.shape)}, expected {first.shape[0]} entries")
+    index = _index(pools[0], f"{what}[0]")
+    entries = pools[0].shape[0] if pools[0].dim() else 0
+    base, size, step = [], [], []
+    for t in pools:
+        if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dim() >= 2 and t.shape[0] == entries):
+            _refuse(t, f"a tensor of {what}", index, None, (entries, "..."))
         es = t.element_size()
         if t.is_contiguous():
-            per = t.numel() // max(1, t.shape[0])
-            dense = True
+            per = t.numel() // max(1, entries)
         else:      # an entry's dimensions in any order, without gaps
-            per, dense = 1, True
+            per = 1
             for st, sz in sorted((t.stride(j), t.shape[j]) for j in range(1, t.dim()) if t.shape[j] > 1):
-                dense &= st == per
+                if st != per:
+                    raise ValueError(f"the entries of {what} must be dense (strides {t.stride()})")
                 per *= sz
-        if not dense:
-            raise ValueError(f"the entries of {what}[{i}] must be dense (strides {t.stride()})")
-        base[i], size[i] = t.data_ptr(), per * es
-        step[i] = t.stride(0) * es if t.shape[0] > 1 else per * es
-    return base, size, step, n, first.shape[0], first.device
+        base.append(t.data_ptr())
+        size.append(per * es)
+        step.append(t.stride(0) * es if entries > 1 else per * es)
+    n = len(base)
+    longs = ctypes.c_int64 * n
+    return (ctypes.c_void_p * n)(*base), longs(*size), longs(*step), n, entries, index
 
 
-def _indices(x, name):
+def _host_ints(x, name):
     """Entry numbers as a host int32 array (a list, tuple or CPU tensor)."""
     if isinstance(x, torch.Tensor):
         if x.is_cuda:
@@ -703,14 +730,15 @@ def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
     """In every pool (tensors [entries, ...] with the same number of entries,
     each entry dense), entry dst[i] becomes a copy of entry src[i]. src and dst
     are host lists; a destination appears once and is no source."""
-    L = load_library()
-    base, size, step, n_pools, n_entries, dev = _entries(pools)
-    a, b = _indices(src, "src"), _indices(dst, "dst")
+    L = _lib or load_library()
+    base, size, step, n_pools, n_entries, index = _entries(pools)
+    a, b = _host_ints(src, "src"), _host_ints(dst, "dst")
     if len(a) != len(b):
         raise ValueError(f"{len(a)} sources for {len(b)} destinations")
-    with _on(dev, stream) as s:
+    with _on(index, stream) as s:
         st = L.jet_cache_copy(base, size, step, n_pools, n_entries, a, b, len(a), s)
-    _check("jet_cache_copy", st)
+    if st:
+        raise JetError("jet_cache_copy", st)
 
 
 def jet_cache_compact_workspace_size(n_pages: int) -> int:
@@ -724,26 +752,28 @@ def jet_cache_compact(pools, page_table, kv_lens, page_size: int, page_table_out
     kv_lens [nseq]) of the pools [pages, ...] to the lowest entries. Returns
     (page_table_out, n_live [1]): the rewritten tables (page_table itself may
     be given) and the number of live pages, on the GPU."""
-    L = load_library()
-    base, size, step, n_pools, n_pages, dev = _entries(pools)
+    L = _lib or load_library()
+    base, size, step, n_pools, n_pages, index = _entries(pools)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [nseq, max_pages]")
-    nseq, max_pages = page_table.shape
-    pt = _ptr_on(page_table, "page_table", dev, torch.int32)
-    kl = _ptr_on(kv_lens, "kv_lens", dev, torch.int32, (nseq,))
-    with _on(dev, stream) as s:
+    shape = page_table.shape
+    nseq, max_pages = shape
+    pt = _dense(page_table, "page_table", index, _I32, shape)
+    kl = _dense(kv_lens, "kv_lens", index, _I32, (nseq,))
+    with _on(index, stream) as s:
         if page_table_out is None:
             page_table_out = torch.empty_like(page_table)
         if n_live is None:
-            n_live = torch.empty(1, device=dev, dtype=torch.int32)
+            n_live = torch.empty(1, device=page_table.device, dtype=_I32)
         if workspace is None:
-            workspace = torch.empty(max(16, L.jet_cache_compact_workspace_size(n_pages)), device=dev,
+            workspace = torch.empty(max(16, L.jet_cache_compact_workspace_size(n_pages)), device=page_table.device,
                                     dtype=torch.uint8)
+        wp, wn = _scratch(workspace, "workspace", index)
         st = L.jet_cache_compact(base, size, step, n_pools, n_pages, page_size, pt, kl, nseq, max_pages,
-                                 _ptr_on(page_table_out, "page_table_out", dev, torch.int32, (nseq, max_pages)),
-                                 _ptr_on(n_live, "n_live", dev, torch.int32, (1,)),
-                                 _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size(), s)
-    _check("jet_cache_compact", st)
+                                 _dense(page_table_out, "page_table_out", index, _I32, shape),
+                                 _dense(n_live, "n_live", index, _I32, (1,)), wp, wn, s)
+    if st:
+        raise JetError("jet_cache_compact", st)
     return page_table_out, n_live
 
 

@@ -90,12 +90,12 @@ attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, 
     return attn::Work{b, c, Hk, G, window, std::max(1, rows / G), gt, (G + gt - 1) / gt, kt, c0, min_chunk};
 }
 
-template <int RW, int SPLIT>
+template <int RW>
 jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
     static_assert(3 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
-    const int per = attn::JOIN_WARPS / SPLIT * RW;
+    const int per = attn::JOIN_WARPS * RW;
     const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
-    return launch(attn::attn_join_kernel<__nv_bfloat16, RW, SPLIT>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
+    return launch(attn::attn_join_kernel<__nv_bfloat16, RW>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
                   (__nv_bfloat16*)o, w.Hk * w.G, d, w.gt);
 }
 
@@ -112,7 +112,7 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::DEC_THREADS), C::SMEM, s, (const __nv_bfloat16*)q,
                                  (long long)q_stride, w, sl, (__nv_bfloat16*)o, d, scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<1, 4>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<1>(w, sl, o, d, n_cta, s);
 }
 
 // pool [n_pages][Hk][page][d] as a 4-D tensor (d, page, Hk, n_pages): a box is 64 columns of up to 128 rows of one page
@@ -162,7 +162,7 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv, tq, w, sl,
                                  (__nv_bfloat16*)o, d,
                                  scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<4, 1>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<4>(w, sl, o, d, n_cta, s);
 }
 
 // rows per sequence and cache head up to which the decode kernel is taken

@@ -226,22 +226,21 @@ __device__ __forceinline__ long long out_row(const Work& w, const Item& it, int 
 // x of the grid takes the item that was cut at the end of CTA x's interval, if
 // it started there. A warp takes RW rows at once, a lane four columns of each;
 // the parts' weights are computed by lanes in parallel, 32 parts at a time,
-// and their rows added with sixteen loads in flight. SPLIT warps share the
-// parts of a row (a long decode's item has a part in every CTA: bound by the
-// latency of its batches of loads) and meet in shared memory.
+// and their rows added with sixteen loads in flight. Bound by latency, and by
+// reading the parts once (a long decode's item has a part in every CTA).
+// Several warps to a row were measured: 2 x 262144 positions 100.6 -> 98.6 us
+// with four, 256 ragged sequences 176 -> 182 us, 64 x 1000 20 -> 24 us for the
+// blocks that find nothing to join.
 constexpr int JOIN_WARPS = 8;
 constexpr int MAX_PARTS = 1024;
 
-template <typename T, int RW, int SPLIT>
+template <typename T, int RW>
 __global__ void __launch_bounds__(JOIN_WARPS * 32, 2)
 attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
-    static_assert(SPLIT == 1 || RW == 1, "one row to a group of warps");
     constexpr int PB = 16 / RW;                             // parts of a batch of loads
-    constexpr int ROWS = JOIN_WARPS / SPLIT * RW;           // rows of a block
+    constexpr int ROWS = JOIN_WARPS * RW;           // rows of a block
     __shared__ int part_slot[MAX_PARTS + PB];
     __shared__ int n_parts;
-    __shared__ float4 meet[SPLIT > 1 ? JOIN_WARPS : 1][32];
-    __shared__ float meet_l[JOIN_WARPS];
     pdl_wait();
     pdl_trigger();
     const int first = blockIdx.x;
@@ -264,7 +263,7 @@ attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
     const int n = n_parts;
     if (n == 0) return;                  // one CTA had all steps after all, and wrote the rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r0 = blockIdx.y * ROWS + warp / SPLIT * RW, share = warp % SPLIT;
+    const int r0 = blockIdx.y * ROWS + warp * RW;
     const bool col = lane * 4 < d;
     const int rmax = min(rows, sl.rows) - 1;
     float M[RW], l[RW], acc[RW][4];
@@ -285,28 +284,27 @@ attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
         for (int m = 16; m > 0; m >>= 1) M[u] = fmaxf(M[u], __shfl_xor_sync(0xffffffffu, M[u], m));
         if (M[u] == -INFINITY) M[u] = 0.f;
     }
-    const int k_begin = n * share / SPLIT, k_end = n * (share + 1) / SPLIT;
 #pragma unroll 1
-    for (int k0 = k_begin; k0 < k_end; k0 += 32) {
+    for (int k0 = 0; k0 < n; k0 += 32) {
         float wt[RW];
 #pragma unroll
         for (int u = 0; u < RW; ++u) {
             wt[u] = 0.f;
-            if (k0 + lane < k_end) {
+            if (k0 + lane < n) {
                 const float2 ml = sl.ml[(long long)part_slot[k0 + lane] * sl.rows + min(r0 + u, rmax)];
                 wt[u] = exp2f(ml.x - M[u]);
                 l[u] += wt[u] * ml.y;
             }
         }
 #pragma unroll 1
-        for (int j = 0; j < min(32, k_end - k0); j += PB) {
+        for (int j = 0; j < min(32, n - k0); j += PB) {
             float4 v[PB][RW];
 #pragma unroll
             for (int p = 0; p < PB; ++p)
 #pragma unroll
                 for (int u = 0; u < RW; ++u) {
                     v[p][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (col && k0 + j + p < k_end)
+                    if (col && k0 + j + p < n)
                         v[p][u] = *reinterpret_cast<const float4*>(
                             sl.o + ((long long)part_slot[k0 + j + p] * sl.rows + min(r0 + u, rmax)) * d + lane * 4);
                 }
@@ -324,21 +322,6 @@ attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
     }
 #pragma unroll
     for (int u = 0; u < RW; ++u) l[u] = warp_sum(l[u]);
-    if (SPLIT > 1) {
-        meet[warp][lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-        if (lane == 0) meet_l[warp] = l[0];
-        __syncthreads();
-        if (share > 0) return;
-#pragma unroll
-        for (int p = 1; p < SPLIT; ++p) {
-            const float4 v = meet[warp + p][lane];
-            acc[0][0] += v.x;
-            acc[0][1] += v.y;
-            acc[0][2] += v.z;
-            acc[0][3] += v.w;
-            l[0] += meet_l[warp + p];
-        }
-    }
 #pragma unroll
     for (int u = 0; u < RW; ++u) {
         const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
