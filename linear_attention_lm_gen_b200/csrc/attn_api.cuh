@@ -60,14 +60,6 @@ jet_status launch_append(const attn::AppendArgs& a, const attn::Cache& c, const 
                 : launch(attn::append_kernel<T, 1, 8>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
 }
 
-template <typename T>
-jet_status launch_attn_simt(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o,
-                            int Hq, int Hk, int d, int window, float scale, cudaStream_t s) {
-    const dim3 grid(b.N, (Hq + attn::SIMT_WARPS - 1) / attn::SIMT_WARPS);
-    return launch(attn::attn_simt_kernel<T>, grid, dim3(attn::SIMT_WARPS * 32), 0, s, (const T*)q,
-                  (long long)q_stride, c, b, (T*)o, Hq, Hk, d, window, scale);
-}
-
 // Workspace of a split attention launch: two slots and a Cut per CTA.
 struct SlotLayout {
     size_t ml, cut, bytes;
@@ -90,13 +82,13 @@ attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, 
     return attn::Work{b, c, Hk, G, window, std::max(1, rows / G), gt, (G + gt - 1) / gt, kt, c0, min_chunk};
 }
 
-template <int RW>
+template <typename T, int RW>
 jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
     static_assert(3 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
     const int per = attn::JOIN_WARPS * RW;
     const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
-    return launch(attn::attn_join_kernel<__nv_bfloat16, RW>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
-                  (__nv_bfloat16*)o, w.Hk * w.G, d, w.gt);
+    return launch(attn::attn_join_kernel<T, RW>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
+                  (T*)o, w.Hk * w.G, d, w.gt);
 }
 
 template <int DP>
@@ -112,7 +104,18 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::DEC_THREADS), C::SMEM, s, (const __nv_bfloat16*)q,
                                  (long long)q_stride, w, sl, (__nv_bfloat16*)o, d, scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<1>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<__nv_bfloat16, 1>(w, sl, o, d, n_cta, s);
+}
+
+jet_status launch_attn_f32(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o, void* ws,
+                           int Hk, int G, int d, int window, float scale, cudaStream_t s) {
+    const int n_cta = launch_sms() * attn::F32_CTAS;
+    const attn::Work w = make_work(c, b, Hk, G, window, attn::F32_ROWS, attn::F32_KT, 96, 192);
+    const attn::Slots sl = make_slots(ws, n_cta, attn::F32_ROWS, d);
+    if (smem_attr(attn::attn_f32_kernel, attn::F32_SMEM) != JET_OK) return JET_ERR_CUDA;
+    const jet_status st = launch(attn::attn_f32_kernel, dim3(n_cta), dim3(attn::F32_THREADS), attn::F32_SMEM, s,
+                                 (const float*)q, (long long)q_stride, w, sl, (float*)o, d, scale * 1.44269504f);
+    return st != JET_OK ? st : launch_join<float, 1>(w, sl, o, d, n_cta, s);
 }
 
 // pool [n_pages][Hk][page][d] as a 4-D tensor (d, page, Hk, n_pages): a box is 64 columns of up to 128 rows of one page
@@ -162,7 +165,7 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv, tq, w, sl,
                                  (__nv_bfloat16*)o, d,
                                  scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<4>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<__nv_bfloat16, 4>(w, sl, o, d, n_cta, s);
 }
 
 // rows per sequence and cache head up to which the decode kernel is taken
@@ -224,7 +227,7 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
 
 size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt) {
     if (check_attn_shape(AttnShape{nseq, N, 1, 1, 16, Hq, Hk, d, dt}) != JET_OK) return 0;
-    if (dt != JET_BF16) return 16;
+    if (dt == JET_F32) return slot_layout(kMaxSMs * attn::F32_CTAS, attn::F32_ROWS, d).bytes;
     const int per_sm = d <= 64 ? attn::DecCfg<64>::CTAS : attn::DecCfg<128>::CTAS;
     return std::max(slot_layout(kMaxSMs * per_sm, attn::DEC_ROWS, d).bytes,
                     slot_layout(kMaxSMs, chunk_rows(Hq / Hk), d).bytes);
@@ -258,7 +261,7 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
                         page_shift_of(page_size)};
     const attn::Batch b{cu_q, kv_lens, nseq, N};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dt == JET_F32) return launch_attn_simt<float>(q, q_stride, c, b, o, Hq, Hk, d, window, scale, s);
+    if (dt == JET_F32) return launch_attn_f32(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
     const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;
     if (typical * (Hq / Hk) > kDecodeRows)
         return d <= 64 ? launch_attn_chunk<1>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)

@@ -22,8 +22,8 @@
 #include "k_attn_chunk.cuh"
 #include "k_attn_common.cuh"
 #include "k_attn_decode.cuh"
+#include "k_attn_f32.cuh"
 #include "k_attn_sched.cuh"
-#include "k_attn_simt.cuh"
 #include "k_cache.cuh"
 #include "k_decode.cuh"
 #include "k_gen.cuh"
