@@ -49,15 +49,18 @@ size_t pool_extent(const AttnShape& a, int64_t page_stride, int64_t head_stride,
                                   (a.page_size - 1) * row_stride + a.d);
 }
 
+template <typename T, int LPR, int E>
+jet_status launch_append_t(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
+    // four tokens to a block once that still fills the GPU several times over
+    if (b.N >= 4 * 4 * kMaxSMs)
+        return launch(attn::append_kernel<T, 4, LPR, E>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+    return launch(attn::append_kernel<T, 1, LPR, E>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+}
 template <typename T>
 jet_status launch_append(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
-    // four tokens to a block once that still fills the GPU several times over
-    const bool wide = b.N >= 4 * 4 * kMaxSMs;
-    if (a.d > 64)
-        return wide ? launch(attn::append_kernel<T, 4, 16>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b)
-                    : launch(attn::append_kernel<T, 1, 16>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
-    return wide ? launch(attn::append_kernel<T, 4, 8>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b)
-                : launch(attn::append_kernel<T, 1, 8>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+    if (a.rot % 16 == 0)
+        return a.d > 64 ? launch_append_t<T, 8, 8>(a, c, b, s) : launch_append_t<T, 4, 8>(a, c, b, s);
+    return a.d > 64 ? launch_append_t<T, 16, 4>(a, c, b, s) : launch_append_t<T, 8, 4>(a, c, b, s);
 }
 
 // Workspace of a split attention launch: two slots and a Cut per CTA.
