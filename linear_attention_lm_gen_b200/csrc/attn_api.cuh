@@ -49,18 +49,19 @@ size_t pool_extent(const AttnShape& a, int64_t page_stride, int64_t head_stride,
                                   (a.page_size - 1) * row_stride + a.d);
 }
 
-template <typename T, int LPR, int E>
+template <typename T, int LPR, int E, bool INTER>
 jet_status launch_append_t(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
     // four tokens to a block once that still fills the GPU several times over
     if (b.N >= 4 * 4 * kMaxSMs)
-        return launch(attn::append_kernel<T, 4, LPR, E>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
-    return launch(attn::append_kernel<T, 1, LPR, E>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
+        return launch(attn::append_kernel<T, 4, LPR, E, INTER>, dim3((b.N + 3) / 4), dim3(attn::APPEND_THREADS), 0, s, a, c,
+                      b);
+    return launch(attn::append_kernel<T, 1, LPR, E, INTER>, dim3(b.N), dim3(attn::APPEND_THREADS), 0, s, a, c, b);
 }
-template <typename T>
+template <typename T, bool INTER>
 jet_status launch_append(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
     if (a.rot % 16 == 0)
-        return a.d > 64 ? launch_append_t<T, 8, 8>(a, c, b, s) : launch_append_t<T, 4, 8>(a, c, b, s);
-    return a.d > 64 ? launch_append_t<T, 16, 4>(a, c, b, s) : launch_append_t<T, 8, 4>(a, c, b, s);
+        return a.d > 64 ? launch_append_t<T, 8, 8, INTER>(a, c, b, s) : launch_append_t<T, 4, 8, INTER>(a, c, b, s);
+    return a.d > 64 ? launch_append_t<T, 16, 4, INTER>(a, c, b, s) : launch_append_t<T, 8, 4, INTER>(a, c, b, s);
 }
 
 // Workspace of a split attention launch: two slots and a Cut per CTA.
@@ -220,12 +221,15 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
             if (overlap(pool, ext, p, n)) return JET_ERR_INVALID_ARG;
     if (k_pool == v_pool) return JET_ERR_INVALID_ARG;
     const attn::AppendArgs args{q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_gamma, k_gamma, inv_freq, q_out,
-                                Hq, Hk, d, rot, interleaved != 0, eps};
+                                Hq, Hk, d, rot, eps};
     const attn::Cache c{k_pool, v_pool, page_stride, head_stride, row_stride, page_table, max_pages, n_pages,
                         page_shift_of(page_size)};
     const attn::Batch b{cu_q, kv_lens, nseq, N};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dt == JET_BF16 ? launch_append<__nv_bfloat16>(args, c, b, s) : launch_append<float>(args, c, b, s);
+    if (dt == JET_BF16)
+        return interleaved ? launch_append<__nv_bfloat16, true>(args, c, b, s)
+                           : launch_append<__nv_bfloat16, false>(args, c, b, s);
+    return interleaved ? launch_append<float, true>(args, c, b, s) : launch_append<float, false>(args, c, b, s);
 }
 
 size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt) {

@@ -6,16 +6,18 @@
 //   pair i is (y_i, y_{i + rot/2}), or (y_2i, y_2i+1) when interleaved
 //
 // Memory-bound: every element is read once and written once. A block takes TB
-// tokens; a group of LPR lanes takes rows (token, head), three of them in
-// flight and the first three on their way before the block looks its sequences
-// up. Each lane has one unit of 2 E elements of a row: E of the first and E of
-// the second half of E rotation pairs, so that a rotation needs no exchange
-// between lanes and the norm LPR lanes' shuffles. E is 8 (16-byte accesses in
-// bf16: half the instructions per element of E = 4, which were the limit there)
-// where the rotated part is a multiple of 16, else 4. The sines are computed
-// once per token and shared through shared memory. The angle is formed and
-// reduced to a fraction of a turn in float64: at position 200000 a float32
-// product would be off by up to 0.008 rad, more than a bf16 step.
+// tokens; a group of LPR lanes takes every S-th row (head) of one token, three
+// of them in flight and the first three on their way before the block looks its
+// sequences up. Each lane has one unit of 2 E elements of a row: E of the first
+// and E of the second half of E rotation pairs, so that a rotation needs no
+// exchange between lanes and the norm LPR lanes' shuffles. E is 8 (16-byte
+// accesses in bf16) where the rotated part is a multiple of 16, else 4. With
+// gammas, sines and cosines multiplied once per token into two coefficients an
+// element, a row costs about 130 instructions a lane; with them applied row by
+// row it took three times that and instructions, not memory, were the limit.
+// The angle is formed and reduced to a fraction of a turn in float64: at
+// position 200000 a float32 product would be off by up to 0.008 rad, more than
+// a bf16 step.
 #pragma once
 #include "k_attn_common.cuh"
 
@@ -29,7 +31,7 @@ struct AppendArgs {
     long long q_stride, k_stride, v_stride, qo_stride;     // elements between tokens
     const float *q_gamma, *k_gamma, *inv_freq;
     void* q_out;
-    int Hq, Hk, d, rot, interleaved;
+    int Hq, Hk, d, rot;
     float eps;
 };
 
@@ -63,21 +65,25 @@ template <typename T, int E> struct Part {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0u;
     }
-    __device__ __forceinline__ void get(float* f) const {
+    // as pairs of consecutive elements
+    __device__ __forceinline__ void get(uint64_t* f) const {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (sizeof(T) == 4) {
-                f[i % E] = __uint_as_float(w[i]);
-            } else {
-                f[(2 * i) % E] = __uint_as_float(w[i] << 16);
-                f[(2 * i + 1) % E] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+        for (int i = 0; i < E / 2; ++i)
+            f[i] = sizeof(T) == 4 ? pair(__uint_as_float(w[(2 * i) % W]), __uint_as_float(w[(2 * i + 1) % W]))
+                                  : pair(__uint_as_float(w[i % W] << 16), __uint_as_float(w[i % W] & 0xffff0000u));
     }
-    __device__ __forceinline__ void put(const float* f) {
+    __device__ __forceinline__ void put(const uint64_t* f) {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            w[i] = sizeof(T) == 4 ? __float_as_uint(f[i % E])
-                                  : Vec16<__nv_bfloat16>::pack2(f[(2 * i) % E], f[(2 * i + 1) % E]);
+        for (int i = 0; i < E / 2; ++i) {
+            float a, b;
+            unpair(f[i], a, b);
+            if (sizeof(T) == 4) {
+                w[(2 * i) % W] = __float_as_uint(a);
+                w[(2 * i + 1) % W] = __float_as_uint(b);
+            } else {
+                w[i % W] = Vec16<__nv_bfloat16>::pack2(a, b);
+            }
+        }
     }
 };
 
@@ -86,55 +92,54 @@ template <int LPR> __device__ __forceinline__ unsigned group_mask() {
     return ((1u << LPR) - 1u) << ((threadIdx.x & 31) / LPR * LPR);
 }
 
-template <typename T, int TB, int LPR, int E>
-__global__ void __launch_bounds__(APPEND_THREADS)
+template <typename T, int TB, int LPR, int E, bool INTER>
+__global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 5 : 4)
 append_kernel(AppendArgs a, Cache c, Batch b) {
-    constexpr int GROUPS = APPEND_THREADS / LPR;
-    constexpr int U = 3;                    // rows in flight per group
-    __shared__ __align__(16) float2 cs[TB][64];
+    constexpr int S = APPEND_THREADS / LPR / TB;            // groups per token
+    constexpr int U = sizeof(T) == 2 ? 3 : 2;               // rows in flight per group
+    __shared__ float2 cs[TB][64];
     __shared__ long long page_off[TB];      // element offset of the token's cache row (head 0), -1: none
     __shared__ int pos[TB];                 // the token's position, -1: it has none
     const int t0 = blockIdx.x * TB;
     const int half = a.rot / 2;
     const int group = threadIdx.x / LPR, unit = threadIdx.x % LPR;
-    const int rpt = a.Hq + 2 * a.Hk;        // rows per token
-    const bool active = unit * 2 * E < a.d;
+    const int u = group / S, first = group % S, t = t0 + u;             // this group's token and first row
+    const int rows = a.Hq + 2 * a.Hk;
+    const bool active = unit * 2 * E < a.d && t < b.N;
     // this lane's 2 E elements: a pair unit of the rotated part, or 2 E elements behind it
     const bool rotated = unit * 2 * E < a.rot;
-    const int e0 = !rotated || a.interleaved ? unit * 2 * E : unit * E;
-    const int e1 = !rotated || a.interleaved ? unit * 2 * E + E : half + unit * E;
-    const int tokens = min(TB, b.N - t0);
+    const int e0 = !rotated || INTER ? unit * 2 * E : unit * E;
+    const int e1 = !rotated || INTER ? unit * 2 * E + E : half + unit * E;
+    const T* qt = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* kt = static_cast<const T*>(a.k) + t * a.k_stride;
+    const T* vt = static_cast<const T*>(a.v) + t * a.v_stride;
     pdl_wait();
     pdl_trigger();
     Part<T, E> x[U][2];
-    auto load = [&](int u, int h) {         // rows (u, h), (u, h + GROUPS) ...
+    auto load = [&](int h) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < U; ++k, h += S) {
             x[k][0].zero();
             x[k][1].zero();
-            if (u < tokens && active) {
-                const int t = t0 + u;
-                const T* src = h < a.Hq ? static_cast<const T*>(a.q) + t * a.q_stride + h * a.d
-                             : h >= a.Hq + a.Hk ? static_cast<const T*>(a.v) + t * a.v_stride + (h - a.Hq - a.Hk) * a.d
-                                                : static_cast<const T*>(a.k) + t * a.k_stride + (h - a.Hq) * a.d;
+            if (active && h < rows) {
+                const T* src = h < a.Hq ? qt + h * a.d : h < a.Hq + a.Hk ? kt + (h - a.Hq) * a.d
+                                                                         : vt + (h - a.Hq - a.Hk) * a.d;
                 x[k][0].load(src + e0);
                 x[k][1].load(src + e1);
             }
-            for (h += GROUPS; h >= rpt; h -= rpt) ++u;
         }
     };
-    int u0 = group / rpt, h0 = group - u0 * rpt;
-    load(u0, h0);                           // on their way while the positions are looked up
+    load(first);                            // on their way while the positions are looked up
     // the sequences of the block's tokens
     const int s0 = block_find_seq(b, t0);
     if (threadIdx.x < TB) {
-        const int t = t0 + threadIdx.x;
+        const int tt = t0 + threadIdx.x;
         int s = s0, p = -1;
-        while (s < b.nseq && b.cu_q[s + 1] <= t) ++s;
+        while (s < b.nseq && b.cu_q[s + 1] <= tt) ++s;
         long long off = -1;
-        if (t < b.N && s < b.nseq) {
+        if (tt < b.N && s < b.nseq) {
             const Seq sq = load_seq(b, c, s, true);
-            const int i = t - sq.r0;
+            const int i = tt - sq.r0;
             if (i >= 0 && i < sq.n) p = max(-1, sq.L - sq.n + i);
             if (p >= 0) {
                 const int pg = load_page(c, s, p);
@@ -146,78 +151,110 @@ append_kernel(AppendArgs a, Cache c, Batch b) {
     }
     __syncthreads();
     for (int e = threadIdx.x; e < TB * half; e += APPEND_THREADS) {
-        const int u = e / half, i = e - u * half;
-        if (pos[u] >= 0) {
+        const int w = e / half, i = e - w * half;
+        if (pos[w] >= 0) {
             // fraction of a turn in float64, its sine and cosine in float32
-            double turn = (double)pos[u] * (double)a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+            double turn = (double)pos[w] * (double)a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
             turn -= rint(turn);
             float sn, cn;
             sincospif((float)(2.0 * turn), &sn, &cn);
-            cs[u][i] = make_float2(cn, sn);
+            cs[w][i] = make_float2(cn, sn);
         }
     }
     __syncthreads();
-    const int rounds = (tokens * rpt + U * GROUPS - 1) / (U * GROUPS);      // the same in every group
-    for (int round = 0; round < rounds; ++round) {
-        if (round > 0) load(u0, h0);
+    if (pos[u] < 0 || t >= b.N) return;     // a whole group
+    // out = own coefficient * element + other coefficient * its partner in the rotation
+    uint64_t own[2][E / 2], other[2][E / 2];
+    auto coefficients = [&](const float* gamma) {
+        if (!active) return;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            float g[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                g[0][j] = gamma ? __ldg(gamma + e0 + 2 * i + j) : 1.f;
+                g[1][j] = gamma ? __ldg(gamma + e1 + 2 * i + j) : 1.f;
+            }
+            if (!rotated) {
+                own[0][i] = pair(g[0][0], g[0][1]);
+                own[1][i] = pair(g[1][0], g[1][1]);
+                other[0][i] = other[1][i] = 0;
+            } else if (INTER) {             // partners: the neighbour
+                const float2 r0 = cs[u][unit * E + i], r1 = cs[u][unit * E + E / 2 + i];
+                own[0][i] = pair(g[0][0] * r0.x, g[0][1] * r0.x);
+                own[1][i] = pair(g[1][0] * r1.x, g[1][1] * r1.x);
+                other[0][i] = pair(-g[0][1] * r0.y, g[0][0] * r0.y);
+                other[1][i] = pair(-g[1][1] * r1.y, g[1][0] * r1.y);
+            } else {                        // partners: the same place of the other half
+                const float2 r0 = cs[u][unit * E + 2 * i], r1 = cs[u][unit * E + 2 * i + 1];
+                own[0][i] = pair(g[0][0] * r0.x, g[0][1] * r1.x);
+                own[1][i] = pair(g[1][0] * r0.x, g[1][1] * r1.x);
+                other[0][i] = pair(-g[1][0] * r0.y, -g[1][1] * r1.y);
+                other[1][i] = pair(g[0][0] * r0.y, g[0][1] * r1.y);
+            }
+        }
+    };
+    bool for_k = first >= a.Hq;
+    coefficients(for_k ? a.k_gamma : a.q_gamma);
+    T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride;
+    const long long off = page_off[u];
+    const float inv_d = 1.f / (float)a.d;
+    for (int h0 = first; h0 < rows; h0 += U * S) {
+        if (h0 > first) load(h0);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int u = min(u0, TB - 1), h = h0, t = t0 + u;
-            const bool on = u0 < tokens && pos[u] >= 0;
-            for (h0 += GROUPS; h0 >= rpt; h0 -= rpt) ++u0;
-            const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hk;
-            if (!on) continue;              // a whole group
-            if (!is_v) {
-                float f0[E], f1[E];
-                x[k][0].get(f0);
-                x[k][1].get(f1);
+            const int h = h0 + k * S;
+            if (h >= rows) break;
+            T* dst = qo + h * a.d;
+            if (h >= a.Hq) {
+                const bool is_v = h >= a.Hq + a.Hk;
+                if (!for_k && !is_v) {
+                    for_k = true;
+                    coefficients(a.k_gamma);
+                }
+                dst = static_cast<T*>(const_cast<void*>(is_v ? c.v : c.k)) + off + (h - a.Hq - (is_v ? a.Hk : 0)) * c.head_stride;
+            }
+            if (h < a.Hq + a.Hk) {
+                uint64_t f[2][E / 2];
+                x[k][0].get(f[0]);
+                x[k][1].get(f[1]);
                 if (a.q_gamma) {
-                    const float* gamma = is_q ? a.q_gamma : a.k_gamma;
-                    float ss = 0.f;
+                    uint64_t sq[2] = {0, 0};
 #pragma unroll
-                    for (int e = 0; e < E; ++e) ss = fmaf(f0[e], f0[e], fmaf(f1[e], f1[e], ss));
+                    for (int i = 0; i < E / 2; ++i) {
+                        sq[0] = fma2(f[0][i], f[0][i], sq[0]);
+                        sq[1] = fma2(f[1][i], f[1][i], sq[1]);
+                    }
+                    float sa, sb;
+                    unpair(add2(sq[0], sq[1]), sa, sb);
+                    float ss = sa + sb;
 #pragma unroll
                     for (int w = LPR / 2; w > 0; w >>= 1) ss += __shfl_xor_sync(group_mask<LPR>(), ss, w);
-                    const float inv = 1.f / sqrtf(ss / (float)a.d + a.eps);
-                    if (active) {
+                    const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+                    const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            f0[e] *= inv * __ldg(gamma + e0 + e);
-                            f1[e] *= inv * __ldg(gamma + e1 + e);
-                        }
+                    for (int i = 0; i < E / 2; ++i) {
+                        f[0][i] = mul2(f[0][i], inv2);
+                        f[1][i] = mul2(f[1][i], inv2);
                     }
                 }
-                if (rotated) {
-                    const float2* tc = cs[u] + unit * E;
-                    if (a.interleaved) {
+                uint64_t y[2][E / 2];
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const float2 ca = tc[e / 2], cb = tc[E / 2 + e / 2];
-                            const float a0 = f0[e], a1 = f0[e + 1], b0 = f1[e], b1 = f1[e + 1];
-                            f0[e] = a0 * ca.x - a1 * ca.y;
-                            f0[e + 1] = a1 * ca.x + a0 * ca.y;
-                            f1[e] = b0 * cb.x - b1 * cb.y;
-                            f1[e + 1] = b1 * cb.x + b0 * cb.y;
-                        }
-                    } else {
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const float4 cc = *reinterpret_cast<const float4*>(tc + e);
-                            const float y0 = f0[e], z0 = f1[e], y1 = f0[e + 1], z1 = f1[e + 1];
-                            f0[e] = y0 * cc.x - z0 * cc.y;
-                            f1[e] = z0 * cc.x + y0 * cc.y;
-                            f0[e + 1] = y1 * cc.z - z1 * cc.w;
-                            f1[e + 1] = z1 * cc.z + y1 * cc.w;
+                    for (int i = 0; i < E / 2; ++i) {
+                        uint64_t partner = f[j ^ 1][i];
+                        if (INTER) {
+                            float lo, hi;
+                            unpair(f[j][i], lo, hi);
+                            partner = pair(hi, lo);
                         }
+                        y[j][i] = fma2(f[j][i], own[j][i], mul2(partner, other[j][i]));
                     }
-                }
-                x[k][0].put(f0);
-                x[k][1].put(f1);
+                x[k][0].put(y[0]);
+                x[k][1].put(y[1]);
             }
-            if (!active || (!is_q && page_off[u] < 0)) continue;
-            T* dst = is_q ? static_cast<T*>(a.q_out) + t * a.qo_stride + h * a.d
-                          : static_cast<T*>(const_cast<void*>(is_v ? c.v : c.k)) + page_off[u] +
-                                (h - a.Hq - (is_v ? a.Hk : 0)) * c.head_stride;
+            if (!active || (h >= a.Hq && off < 0)) continue;
             x[k][0].store(dst + e0);
             x[k][1].store(dst + e1);
         }
