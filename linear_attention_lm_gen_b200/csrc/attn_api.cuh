@@ -102,7 +102,7 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     const int n_cta = launch_sms() * C::CTAS;
     // an item's start and end cost a CTA about as much as 96 positions; parts
     // below 256 positions are not worth joining
-    const attn::Work w = make_work(c, b, Hk, G, window, attn::DEC_ROWS, attn::DEC_KT, 96, 256);
+    const attn::Work w = make_work(c, b, Hk, G, window, attn::DEC_ROWS, attn::DEC_KT, 192, 128);
     const attn::Slots sl = make_slots(ws, n_cta, attn::DEC_ROWS, d);
     auto kern = attn::attn_decode_kernel<DP>;
     if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
@@ -158,7 +158,7 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
                              void* ws, int Hk, int G, int d, int window, float scale, cudaStream_t s) {
     typedef attn::ChSmem<NB> SM;
     const int n_cta = launch_sms(), rows = chunk_rows(G);
-    attn::Work w = make_work(c, b, Hk, G, window, rows, attn::CH_KT, 256, 384);
+    attn::Work w = make_work(c, b, Hk, G, window, rows, attn::CH_KT, 384, 384);
     w.tpt = 2 * (128 / G);
     const attn::Slots sl = make_slots(ws, n_cta, rows, d);
     CUtensorMap tk, tv, tq;

@@ -6,15 +6,15 @@
 //   pair i is (y_i, y_{i + rot/2}), or (y_2i, y_2i+1) when interleaved
 //
 // Memory-bound: every element is read once and written once. A block takes TB
-// tokens; a group of LPR lanes takes every S-th row (head) of one token, three
-// of them in flight and the first three on their way before the block looks its
+// tokens; a group of LPR lanes takes every S-th row (head) of one token, two
+// of them in flight and the first two on their way before the block looks its
 // sequences up. Each lane has one unit of 2 E elements of a row: E of the first
 // and E of the second half of E rotation pairs, so that a rotation needs no
 // exchange between lanes and the norm LPR lanes' shuffles. E is 8 (16-byte
-// accesses in bf16) where the rotated part is a multiple of 16, else 4. With
-// gammas, sines and cosines multiplied once per token into two coefficients an
-// element, a row costs about 130 instructions a lane; with them applied row by
-// row it took three times that and instructions, not memory, were the limit.
+// accesses in bf16) where the rotated part is a multiple of 16, else 4. Gammas,
+// cosines and sines are multiplied once per token into two coefficients an
+// element, kept in shared memory: applied row by row they made instructions the
+// limit, and in registers the occupancy.
 // The angle is formed and reduced to a fraction of a turn in float64: at
 // position 200000 a float32 product would be off by up to 0.008 rad, more than
 // a bf16 step.
@@ -93,11 +93,14 @@ template <int LPR> __device__ __forceinline__ unsigned group_mask() {
 }
 
 template <typename T, int TB, int LPR, int E, bool INTER>
-__global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 5 : 4)
+__global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 8 : 6)
 append_kernel(AppendArgs a, Cache c, Batch b) {
     constexpr int S = APPEND_THREADS / LPR / TB;            // groups per token
-    constexpr int U = sizeof(T) == 2 ? 3 : 2;               // rows in flight per group
-    __shared__ float2 cs[TB][64];
+    constexpr int U = 2;                                    // rows in flight per group
+    // out = own * element + other * its partner in the rotation: the gammas times the
+    // cosines and sines, for queries (0) and keys (1) of each token
+    __shared__ __align__(16) float own[TB][2][128], other[TB][2][128];
+    __shared__ float gs[2][128], fs[64];
     __shared__ long long page_off[TB];      // element offset of the token's cache row (head 0), -1: none
     __shared__ int pos[TB];                 // the token's position, -1: it has none
     const int t0 = blockIdx.x * TB;
@@ -129,73 +132,59 @@ append_kernel(AppendArgs a, Cache c, Batch b) {
             }
         }
     };
-    load(first);                            // on their way while the positions are looked up
+    // on their way while the positions are looked up
+    load(first);
+    if ((int)threadIdx.x < a.d) {
+        gs[0][threadIdx.x] = a.q_gamma ? a.q_gamma[threadIdx.x] : 1.f;
+        gs[1][threadIdx.x] = a.q_gamma ? a.k_gamma[threadIdx.x] : 1.f;
+    }
+    if ((int)threadIdx.x < half) fs[threadIdx.x] = a.inv_freq[threadIdx.x];
     // the sequences of the block's tokens
     const int s0 = block_find_seq(b, t0);
+    int s = s0, p = -1;
     if (threadIdx.x < TB) {
         const int tt = t0 + threadIdx.x;
-        int s = s0, p = -1;
         while (s < b.nseq && b.cu_q[s + 1] <= tt) ++s;
-        long long off = -1;
         if (tt < b.N && s < b.nseq) {
             const Seq sq = load_seq(b, c, s, true);
             const int i = tt - sq.r0;
             if (i >= 0 && i < sq.n) p = max(-1, sq.L - sq.n + i);
-            if (p >= 0) {
-                const int pg = load_page(c, s, p);
-                if (pg >= 0) off = pg * c.page_stride + (p & ((1 << c.page_shift) - 1)) * c.row_stride;
-            }
         }
         pos[threadIdx.x] = p;
-        page_off[threadIdx.x] = off;
     }
     __syncthreads();
+    const int pg = p >= 0 ? load_page(c, s, p) : -1;        // needed only when the rows are stored
     for (int e = threadIdx.x; e < TB * half; e += APPEND_THREADS) {
         const int w = e / half, i = e - w * half;
         if (pos[w] >= 0) {
             // fraction of a turn in float64, its sine and cosine in float32
-            double turn = (double)pos[w] * (double)a.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+            double turn = (double)pos[w] * (double)fs[i] * 0.15915494309189533577;   // 1 / (2 pi)
             turn -= rint(turn);
             float sn, cn;
             sincospif((float)(2.0 * turn), &sn, &cn);
-            cs[w][i] = make_float2(cn, sn);
+            const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + half;       // the pair
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const float ga = gs[z][ia], gb = gs[z][ib];
+                own[w][z][ia] = ga * cn;
+                own[w][z][ib] = gb * cn;
+                other[w][z][ia] = -gb * sn;
+                other[w][z][ib] = ga * sn;
+            }
         }
     }
+    for (int e = a.rot + threadIdx.x; e < a.d; e += APPEND_THREADS)
+#pragma unroll
+        for (int w = 0; w < TB; ++w)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                own[w][z][e] = gs[z][e];
+                other[w][z][e] = 0.f;
+            }
+    if (threadIdx.x < TB)
+        page_off[threadIdx.x] = pg >= 0 ? pg * c.page_stride + (p & ((1 << c.page_shift) - 1)) * c.row_stride : -1;
     __syncthreads();
     if (pos[u] < 0 || t >= b.N) return;     // a whole group
-    // out = own coefficient * element + other coefficient * its partner in the rotation
-    uint64_t own[2][E / 2], other[2][E / 2];
-    auto coefficients = [&](const float* gamma) {
-        if (!active) return;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float g[2][2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                g[0][j] = gamma ? __ldg(gamma + e0 + 2 * i + j) : 1.f;
-                g[1][j] = gamma ? __ldg(gamma + e1 + 2 * i + j) : 1.f;
-            }
-            if (!rotated) {
-                own[0][i] = pair(g[0][0], g[0][1]);
-                own[1][i] = pair(g[1][0], g[1][1]);
-                other[0][i] = other[1][i] = 0;
-            } else if (INTER) {             // partners: the neighbour
-                const float2 r0 = cs[u][unit * E + i], r1 = cs[u][unit * E + E / 2 + i];
-                own[0][i] = pair(g[0][0] * r0.x, g[0][1] * r0.x);
-                own[1][i] = pair(g[1][0] * r1.x, g[1][1] * r1.x);
-                other[0][i] = pair(-g[0][1] * r0.y, g[0][0] * r0.y);
-                other[1][i] = pair(-g[1][1] * r1.y, g[1][0] * r1.y);
-            } else {                        // partners: the same place of the other half
-                const float2 r0 = cs[u][unit * E + 2 * i], r1 = cs[u][unit * E + 2 * i + 1];
-                own[0][i] = pair(g[0][0] * r0.x, g[0][1] * r1.x);
-                own[1][i] = pair(g[1][0] * r0.x, g[1][1] * r1.x);
-                other[0][i] = pair(-g[1][0] * r0.y, -g[1][1] * r1.y);
-                other[1][i] = pair(g[0][0] * r0.y, g[0][1] * r1.y);
-            }
-        }
-    };
-    bool for_k = first >= a.Hq;
-    coefficients(for_k ? a.k_gamma : a.q_gamma);
     T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride;
     const long long off = page_off[u];
     const float inv_d = 1.f / (float)a.d;
@@ -208,10 +197,6 @@ append_kernel(AppendArgs a, Cache c, Batch b) {
             T* dst = qo + h * a.d;
             if (h >= a.Hq) {
                 const bool is_v = h >= a.Hq + a.Hk;
-                if (!for_k && !is_v) {
-                    for_k = true;
-                    coefficients(a.k_gamma);
-                }
                 dst = static_cast<T*>(const_cast<void*>(is_v ? c.v : c.k)) + off + (h - a.Hq - (is_v ? a.Hk : 0)) * c.head_stride;
             }
             if (h < a.Hq + a.Hk) {
@@ -238,18 +223,26 @@ append_kernel(AppendArgs a, Cache c, Batch b) {
                         f[1][i] = mul2(f[1][i], inv2);
                     }
                 }
+                const float* po = own[u][h < a.Hq ? 0 : 1];
+                const float* pt = other[u][h < a.Hq ? 0 : 1];
                 uint64_t y[2][E / 2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < E / 2; ++i) {
-                        uint64_t partner = f[j ^ 1][i];
+                    for (int i = 0; i < E / 2; i += 2) {
+                        const int e = (j ? e1 : e0) + 2 * i;
+                        const ulonglong2 co = *reinterpret_cast<const ulonglong2*>(po + e);
+                        const ulonglong2 cp = *reinterpret_cast<const ulonglong2*>(pt + e);
+                        uint64_t pa = f[j ^ 1][i], pb = f[j ^ 1][i + 1];
                         if (INTER) {
                             float lo, hi;
                             unpair(f[j][i], lo, hi);
-                            partner = pair(hi, lo);
+                            pa = pair(hi, lo);
+                            unpair(f[j][i + 1], lo, hi);
+                            pb = pair(hi, lo);
                         }
-                        y[j][i] = fma2(f[j][i], own[j][i], mul2(partner, other[j][i]));
+                        y[j][i] = fma2(f[j][i], co.x, mul2(pa, cp.x));
+                        y[j][i + 1] = fma2(f[j][i + 1], co.y, mul2(pb, cp.y));
                     }
                 x[k][0].put(y[0]);
                 x[k][1].put(y[1]);
