@@ -100,8 +100,8 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
                               void* ws, int Hk, int G, int d, int window, float scale, cudaStream_t s) {
     typedef attn::DecCfg<DP> C;
     const int n_cta = launch_sms() * C::CTAS;
-    // an item's start and end cost a CTA about as much as 96 positions; parts
-    // below 256 positions are not worth joining
+    // an item's start and end cost a CTA about as much as 192 positions; parts
+    // below 128 positions are not worth joining
     const attn::Work w = make_work(c, b, Hk, G, window, attn::DEC_ROWS, attn::DEC_KT, 192, 128);
     const attn::Slots sl = make_slots(ws, n_cta, attn::DEC_ROWS, d);
     auto kern = attn::attn_decode_kernel<DP>;
