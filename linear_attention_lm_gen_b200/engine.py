@@ -18,6 +18,8 @@ the library's calls on them:
                the tensor-core path batch pieces of equal length instead)
   decode(seqs, ...)  one new token for each of a batch of sequences, in place
                on their entries (jet_jetblock_decode_slots)
+  fork(seq, children)  sequences that continue from seq: their entries are
+               copies of its state and history (jet_cache_copy, one launch)
   release(seq) return the entry
   submit(seq, prompt) / step(tokens)  a serving iteration: up to
                `chunk_tokens` queued prompt tokens (oldest prompt first; a
@@ -35,7 +37,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (jet_jetblock_decode_slots, jet_jetblock_prefill, jet_jetblock_prefill_varlen,
+from . import (jet_cache_copy, jet_jetblock_decode_slots, jet_jetblock_prefill, jet_jetblock_prefill_varlen,
                jet_jetblock_prefill_workspace_size)
 
 MAX_VARLEN_SEQS = 256    # sequences per variable-length call
@@ -76,6 +78,24 @@ class JetEngine:
         self.slot[seq] = s
         self.pos[seq] = 0
         return s
+
+    def fork(self, seq, children) -> None:
+        """Admit `children` as continuations of `seq` (parallel samples or
+        beams): each gets a pool entry with a copy of its state and history."""
+        children = list(children)
+        if seq not in self.slot:
+            raise KeyError(f"sequence {seq!r} is not admitted")
+        if seq in self.prefilling:
+            raise ValueError(f"sequence {seq!r} is still in prefill")
+        if len(set(children)) != len(children) or any(c in self.slot for c in children):
+            raise KeyError("a child is already admitted or appears twice")
+        if len(children) > len(self._free):
+            raise RuntimeError("state cache is full")
+        dst = [self._free.pop() for _ in children]
+        jet_cache_copy([self.S, self.hist], [self.slot[seq]] * len(dst), dst)
+        for c, s in zip(children, dst):
+            self.slot[c] = s
+            self.pos[c] = self.pos[seq]
 
     def release(self, seq) -> None:
         self._free.append(self.slot.pop(seq))
