@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -537,6 +538,14 @@ class _on:
         return False
 
 
+def _issue(index, stream, call):
+    """call(raw stream) with GPU `index` current, on its current stream unless one is given."""
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with _on(index, stream) as s:
+        return call(s)
+
+
 def _refuse(t, name, index, dtype, shape):
     """Raise what is wrong with an argument that has to be a tensor of this dtype and shape on GPU `index`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -558,10 +567,12 @@ def _index(t, name):
 
 def _dense(t, name, index, dtype, shape):
     """Address of a contiguous tensor of this dtype and shape on GPU `index`."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
-        _refuse(t, name, index, dtype, shape)
-    return t.data_ptr()
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, index, dtype, shape)
 
 
 def _scratch(t, name, index):
@@ -638,15 +649,16 @@ def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, pag
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         fr = _dense(inv_freq, "inv_freq", index, torch.float32, (rot // 2,))
-    with _on(index, stream) as s:
-        if q_out is None:
-            q_out = torch.empty((N, Hq, d), device=q.device, dtype=dt)
-        op, os_ = _rows(q_out, "q_out", index, dt, shape)
+
+    def call(s):
+        out = torch.empty((N, Hq, d), device=q.device, dtype=dt) if q_out is None else q_out
+        op, os_ = _rows(out, "q_out", index, dt, shape)
         st = L.jet_attn_rope_append(qp, qs, kp, ks, vp, vs, gq, gk, eps, fr, rot, 1 if interleaved else 0, op, os_, kpool,
                                     vpool, ps, hs, rs, cu, kl, pt, nseq, N, max_pages, n_pages, page, Hq, Hk, d, code, s)
-    if st:
-        raise JetError("jet_attn_rope_append", st)
-    return q_out
+        if st:
+            raise JetError("jet_attn_rope_append", st)
+        return out
+    return _issue(index, stream, call)
 
 
 def jet_attn_paged_workspace_size(nseq: int, N: int, Hq: int, Hk: int, d: int, dtype=torch.bfloat16) -> int:
@@ -673,19 +685,21 @@ def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 
     qp, qs = _rows(q, "q", index, dt, shape)
     kpool, vpool, ps, hs, rs, n_pages, page = _kv_pools(k_pool, v_pool, index, dt, Hk, d)
     cu, kl, pt, nseq, max_pages = _batch(cu_q, kv_lens, page_table, index)
-    with _on(index, stream) as s:
-        if o is None:
-            o = torch.empty((N, Hq, d), device=q.device, dtype=dt)
-        if workspace is None:
-            workspace = torch.empty(max(16, L.jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, code)), device=q.device,
-                                    dtype=torch.uint8)
-        wp, wn = _scratch(workspace, "workspace", index)
-        st = L.jet_attn_paged(qp, qs, kpool, vpool, ps, hs, rs, cu, kl, pt, _dense(o, "o", index, dt, shape), wp, wn,
+
+    def call(s):
+        out = torch.empty((N, Hq, d), device=q.device, dtype=dt) if o is None else o
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(16, L.jet_attn_paged_workspace_size(nseq, N, Hq, Hk, d, code)), device=q.device,
+                             dtype=torch.uint8)
+        wp, wn = _scratch(ws, "workspace", index)
+        st = L.jet_attn_paged(qp, qs, kpool, vpool, ps, hs, rs, cu, kl, pt, _dense(out, "o", index, dt, shape), wp, wn,
                               nseq, N, max_new, max_pages, n_pages, page, Hq, Hk, d, window,
                               d ** -0.5 if scale is None else scale, code, s)
-    if st:
-        raise JetError("jet_attn_paged", st)
-    return o
+        if st:
+            raise JetError("jet_attn_paged", st)
+        return out
+    return _issue(index, stream, call)
 
 
 # ---------------------------------------------------------------- cache entries
@@ -695,9 +709,16 @@ def _entries(pools, what="pools"):
     if isinstance(pools, torch.Tensor) or len(pools) == 0:
         raise TypeError(f"{what} must be a non-empty list of tensors")
     index = _index(pools[0], f"{what}[0]")
-    entries = pools[0].shape[0] if pools[0].dim() else 0
+    shape, dtype = pools[0].shape, pools[0].dtype
+    entries = shape[0] if len(shape) else 0
     base, size, step = [], [], []
     for t in pools:
+        if base and isinstance(t, torch.Tensor) and t.get_device() == index and t.shape == shape and t.dtype is dtype \
+                and t.stride() == stride:        # laid out as the first one
+            base.append(t.data_ptr())
+            size.append(size[0])
+            step.append(step[0])
+            continue
         if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dim() >= 2 and t.shape[0] == entries):
             _refuse(t, f"a tensor of {what}", index, None, (entries, "..."))
         es = t.element_size()
@@ -709,12 +730,12 @@ def _entries(pools, what="pools"):
                 if st != per:
                     raise ValueError(f"the entries of {what} must be dense (strides {t.stride()})")
                 per *= sz
+        if not base:
+            stride = t.stride()
         base.append(t.data_ptr())
         size.append(per * es)
         step.append(t.stride(0) * es if entries > 1 else per * es)
-    n = len(base)
-    longs = ctypes.c_int64 * n
-    return (ctypes.c_void_p * n)(*base), longs(*size), longs(*step), n, entries, index
+    return array("q", base), array("q", size), array("q", step), len(base), entries, index
 
 
 def _host_ints(x, name):
@@ -723,7 +744,12 @@ def _host_ints(x, name):
         if x.is_cuda:
             raise TypeError(f"{name} must be on the host: it is checked before the launch")
         x = x.tolist()
-    return (ctypes.c_int * len(x))(*x)
+    return array("i", x)
+
+
+def _at(a):
+    """Address of a host array."""
+    return a.buffer_info()[0] if len(a) else None
 
 
 def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
@@ -735,8 +761,8 @@ def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
     a, b = _host_ints(src, "src"), _host_ints(dst, "dst")
     if len(a) != len(b):
         raise ValueError(f"{len(a)} sources for {len(b)} destinations")
-    with _on(index, stream) as s:
-        st = L.jet_cache_copy(base, size, step, n_pools, n_entries, a, b, len(a), s)
+    st = _issue(index, stream, lambda s: L.jet_cache_copy(_at(base), _at(size), _at(step), n_pools, n_entries, _at(a),
+                                                          _at(b), len(a), s))
     if st:
         raise JetError("jet_cache_copy", st)
 
@@ -760,21 +786,22 @@ def jet_cache_compact(pools, page_table, kv_lens, page_size: int, page_table_out
     nseq, max_pages = shape
     pt = _dense(page_table, "page_table", index, _I32, shape)
     kl = _dense(kv_lens, "kv_lens", index, _I32, (nseq,))
-    with _on(index, stream) as s:
-        if page_table_out is None:
-            page_table_out = torch.empty_like(page_table)
-        if n_live is None:
-            n_live = torch.empty(1, device=page_table.device, dtype=_I32)
-        if workspace is None:
-            workspace = torch.empty(max(16, L.jet_cache_compact_workspace_size(n_pages)), device=page_table.device,
-                                    dtype=torch.uint8)
-        wp, wn = _scratch(workspace, "workspace", index)
-        st = L.jet_cache_compact(base, size, step, n_pools, n_pages, page_size, pt, kl, nseq, max_pages,
-                                 _dense(page_table_out, "page_table_out", index, _I32, shape),
-                                 _dense(n_live, "n_live", index, _I32, (1,)), wp, wn, s)
-    if st:
-        raise JetError("jet_cache_compact", st)
-    return page_table_out, n_live
+
+    def call(s):
+        out = torch.empty_like(page_table) if page_table_out is None else page_table_out
+        live = torch.empty(1, device=page_table.device, dtype=_I32) if n_live is None else n_live
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(16, L.jet_cache_compact_workspace_size(n_pages)), device=page_table.device,
+                             dtype=torch.uint8)
+        wp, wn = _scratch(ws, "workspace", index)
+        st = L.jet_cache_compact(_at(base), _at(size), _at(step), n_pools, n_pages, page_size, pt, kl, nseq, max_pages,
+                                 _dense(out, "page_table_out", index, _I32, shape),
+                                 _dense(live, "n_live", index, _I32, (1,)), wp, wn, s)
+        if st:
+            raise JetError("jet_cache_compact", st)
+        return out, live
+    return _issue(index, stream, call)
 
 
 def jet_device_error(stream=None) -> int:

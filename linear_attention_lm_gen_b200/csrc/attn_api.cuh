@@ -86,13 +86,13 @@ attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, 
     return attn::Work{b, c, Hk, G, window, std::max(1, rows / G), gt, (G + gt - 1) / gt, kt, c0, min_chunk};
 }
 
-template <typename T, int RW>
+template <typename T, int RW, int PB, int BLOCKS>
 jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
     static_assert(3 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
     const int per = attn::JOIN_WARPS * RW;
     const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
-    return launch(attn::attn_join_kernel<T, RW>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl,
-                  (T*)o, w.Hk * w.G, d, w.gt);
+    return launch(attn::attn_join_kernel<T, RW, PB, BLOCKS>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl, (T*)o, w.Hk * w.G,
+                  d, w.gt);
 }
 
 template <int DP>
@@ -108,7 +108,7 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::DEC_THREADS), C::SMEM, s, (const __nv_bfloat16*)q,
                                  (long long)q_stride, w, sl, (__nv_bfloat16*)o, d, scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<__nv_bfloat16, 1>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<__nv_bfloat16, 1, 16, 2>(w, sl, o, d, n_cta, s);
 }
 
 jet_status launch_attn_f32(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o, void* ws,
@@ -119,7 +119,7 @@ jet_status launch_attn_f32(const void* q, int64_t q_stride, const attn::Cache& c
     if (smem_attr(attn::attn_f32_kernel, attn::F32_SMEM) != JET_OK) return JET_ERR_CUDA;
     const jet_status st = launch(attn::attn_f32_kernel, dim3(n_cta), dim3(attn::F32_THREADS), attn::F32_SMEM, s,
                                  (const float*)q, (long long)q_stride, w, sl, (float*)o, d, scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<float, 1>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<float, 1, 16, 2>(w, sl, o, d, n_cta, s);
 }
 
 // pool [n_pages][Hk][page][d] as a 4-D tensor (d, page, Hk, n_pages): a box is 64 columns of up to 128 rows of one page
@@ -169,7 +169,7 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
     const jet_status st = launch(kern, dim3(n_cta), dim3(attn::CH_THREADS), SM::BYTES, s, tk, tv, tq, w, sl,
                                  (__nv_bfloat16*)o, d,
                                  scale * 1.44269504f);
-    return st != JET_OK ? st : launch_join<__nv_bfloat16, 4>(w, sl, o, d, n_cta, s);
+    return st != JET_OK ? st : launch_join<__nv_bfloat16, 4, 2, 4>(w, sl, o, d, n_cta, s);
 }
 
 // rows per sequence and cache head up to which the decode kernel is taken

@@ -226,19 +226,18 @@ __device__ __forceinline__ long long out_row(const Work& w, const Item& it, int 
 // x of the grid takes the item that was cut at the end of CTA x's interval, if
 // it started there. A warp takes RW rows at once, a lane four columns of each;
 // the parts' weights are computed by lanes in parallel, 32 parts at a time,
-// and their rows added with sixteen loads in flight. Bound by latency, and by
-// reading the parts once (a long decode's item has a part in every CTA).
-// Several warps to a row were measured: 2 x 262144 positions 100.6 -> 98.6 us
-// with four, 256 ragged sequences 176 -> 182 us, 64 x 1000 20 -> 24 us for the
-// blocks that find nothing to join.
+// and their rows added PB parts at a time, all their loads in flight. Bound by
+// latency, and by reading the parts once: a chunk's item has two or three
+// parts of up to 256 rows (RW 4, PB 2, four blocks to an SM: 4096 new tokens
+// 87 -> 81 us against PB 4 and two blocks), a decode's up to one part per CTA
+// of few rows (RW 1, PB 16). Several warps to a row were measured: 2 x 262144
+// positions gain 2 us, 64 x 1000 lose 1 to 4 us to the larger grid.
 constexpr int JOIN_WARPS = 8;
 constexpr int MAX_PARTS = 1024;
 
-template <typename T, int RW>
-__global__ void __launch_bounds__(JOIN_WARPS * 32, 2)
+template <typename T, int RW, int PB, int BLOCKS>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, BLOCKS)
 attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
-    constexpr int PB = 16 / RW;                             // parts of a batch of loads
-    constexpr int ROWS = JOIN_WARPS * RW;           // rows of a block
     __shared__ int part_slot[MAX_PARTS + PB];
     __shared__ int n_parts;
     pdl_wait();
@@ -247,7 +246,7 @@ attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
     const Cut me = sl.cut[first];
     if (me.last <= first) return;
     const int rows = me.nt * gt;
-    if ((int)blockIdx.y * ROWS >= rows) return;
+    if ((int)blockIdx.y * JOIN_WARPS * RW >= rows) return;
     if (threadIdx.x < 32) {
         int n = 0;
         for (int k0 = first; k0 <= me.last; k0 += 32) {
@@ -263,7 +262,7 @@ attn_join_kernel(Slots sl, T* __restrict__ o, int Hq, int d, int gt) {
     const int n = n_parts;
     if (n == 0) return;                  // one CTA had all steps after all, and wrote the rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r0 = blockIdx.y * ROWS + warp * RW;
+    const int r0 = (blockIdx.y * JOIN_WARPS + warp) * RW;
     const bool col = lane * 4 < d;
     const int rmax = min(rows, sl.rows) - 1;
     float M[RW], l[RW], acc[RW][4];
