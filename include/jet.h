@@ -423,7 +423,8 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
  *   be replayed with other lengths):
  *   cu_q [nseq + 1]: the new tokens of sequence s are rows cu_q[s] ..
  *     cu_q[s+1]-1 of the packed tensors (a sequence may have none; rows from
- *     cu_q[nseq] up to N are padding and are neither read nor written);
+ *     cu_q[nseq] up to N are padding: no result depends on them and they are
+ *     not written);
  *   kv_lens [nseq]: positions of s, the new tokens included: new token i of
  *     n is at position kv_lens[s] - n + i;
  *   page_table [nseq][max_pages]: pages of s; entries that no call reaches
@@ -434,7 +435,7 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
  *   the device error word (JET_ERR_DEVICE from jet_device_error).
  * Shapes: Hq a multiple of Hk (head h of q reads head h / (Hq / Hk) of the
  *   cache), Hq <= 256, Hq / Hk <= 64; d a multiple of 16, at most 128;
- *   nseq <= 65535; max_pages * page_size at most 2^30 and N at most 2^24.
+ *   nseq <= 65535; max_pages * page_size at most 2^30, N at most 2^24.
  * q, k, v and the pools have the storage type dt (JET_BF16 or JET_F32); all
  * arithmetic is float32, results are rounded once.
  * ---------------------------------------------------------------------- */

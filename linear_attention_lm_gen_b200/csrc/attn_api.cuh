@@ -11,6 +11,8 @@ struct AttnShape {
     jet_dtype dt;
 };
 
+constexpr int64_t kMaxTokenStride = 1LL << 32;      // elements between tokens of q, k, v (with N <= 2^24: spans fit)
+
 jet_status check_attn_shape(const AttnShape& a) {
     if (!dtype_ok(a.dt)) return JET_ERR_INVALID_ARG;
     if (a.nseq <= 0 || a.N <= 0 || a.max_pages <= 0 || a.n_pages <= 0 || a.page_size <= 0 || a.Hq <= 0 || a.Hk <= 0 ||
@@ -39,6 +41,7 @@ jet_status check_pools(const AttnShape& a, const void* k, const void* v, int64_t
         if (st < a.d || st > (1LL << 38)) return JET_ERR_INVALID_ARG;
         if (st % align != 0) return JET_ERR_MISALIGNED;
     }
+    if (elems({a.n_pages, page_stride}) < 0 || elems({a.n_pages, page_stride}) > (1LL << 60)) return JET_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v)) return JET_ERR_MISALIGNED;
     return JET_OK;
 }
@@ -195,10 +198,9 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
     if (q_gamma && !(eps >= 0.f && eps < INFINITY)) return JET_ERR_INVALID_ARG;
     if (rot % 8 != 0) return JET_ERR_UNSUPPORTED;
     const size_t es = esize(dt);
-    const int64_t kMaxStride = 1LL << 38;
     for (auto [sd, heads] : {std::pair<int64_t, int>{q_stride, Hq}, {k_stride, Hk}, {v_stride, Hk},
                              {q_out_stride, Hq}}) {
-        if (sd < (int64_t)heads * d || sd > kMaxStride) return JET_ERR_INVALID_ARG;
+        if (sd < (int64_t)heads * d || sd > kMaxTokenStride) return JET_ERR_INVALID_ARG;
         if (sd % 8 != 0) return JET_ERR_MISALIGNED;
     }
     st = check_pools(a, k_pool, v_pool, page_stride, head_stride, row_stride);
@@ -250,7 +252,7 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
     jet_status st = check_attn_shape(a);
     if (st != JET_OK) return st;
     if (window < 0 || max_new < 0 || !(scale > 0.f && scale < INFINITY)) return JET_ERR_INVALID_ARG;
-    if (q_stride < (int64_t)Hq * d || q_stride > (1LL << 38)) return JET_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)Hq * d || q_stride > kMaxTokenStride) return JET_ERR_INVALID_ARG;
     if (q_stride % 8 != 0) return JET_ERR_MISALIGNED;
     st = check_pools(a, k_pool, v_pool, page_stride, head_stride, row_stride);
     if (st != JET_OK) return st;

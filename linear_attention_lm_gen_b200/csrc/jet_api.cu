@@ -1322,4 +1322,8 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
 extern "C" int jet_test_skip_p2a(int on) {
     return cudaMemcpyToSymbol(jet::pfch::g_test_skip_p2a, &on, sizeof(int)) == cudaSuccess ? 0 : 1;
 }
+// test builds only: see g_test_skip_scores
+extern "C" int jet_test_skip_scores(int on) {
+    return cudaMemcpyToSymbol(jet::attn::g_test_skip_scores, &on, sizeof(int)) == cudaSuccess ? 0 : 1;
+}
 #endif

@@ -128,13 +128,13 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
     const uint64_t t0 = global_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;        // suspends the thread for a while by itself
         if ((i & 15u) == 0) {
             if (*abort_flag) return false;
-            if (global_ns() - t0 > kWaitLimitNs) break;
+            if (global_ns() - t0 > limit_ns) break;
         }
     }
     *abort_flag = 1;
@@ -143,7 +143,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 }
 // Wait for a phase, bounded in time; false once any role gave up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag);
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag, kWaitLimitNs);
 }
 
 // What the roles need of an item, as the queue holds it.
@@ -159,6 +159,11 @@ struct ChItem {
 };
 constexpr int CH_QUEUE = 4;
 constexpr int CH_READERS = 11;      // warps that read the queue: softmax, products, loads, V
+
+#ifdef JET_TEST_WAIT_EXPIRY
+// test builds only: leave out the first scores of tile A, so that the wait for them runs out
+__device__ int g_test_skip_scores;
+#endif
 
 template <int NB>
 __global__ void __launch_bounds__(CH_THREADS, 1)
@@ -456,6 +461,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (!wait(B::Q, phQ)) break;
             phQ ^= 1;
             tc_fence_after();
+#ifdef JET_TEST_WAIT_EXPIRY
+            if (!*reinterpret_cast<volatile int*>(&g_test_skip_scores))
+#endif
             issue_s(0, slot);
             if (two) issue_s(1, slot);
             release(B::EMPTY + slot);
@@ -618,7 +626,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             note_item(w, it, blockIdx.x, x0, x1, chunk, b0, b1, cut)};
             }
             if (mine) {
-                if (n_it >= CH_QUEUE) ok = wait_for(&bars[B::IE + k], (n_it / CH_QUEUE - 1) & 1, abort_flag);
+                // the others may be at work on one long item all the while: a longer limit, and their own ends it too
+                if (n_it >= CH_QUEUE)
+                    ok = wait_on(&bars[B::IE + k], (n_it / CH_QUEUE - 1) & 1, abort_flag, 64 * kWaitLimitNs);
                 if (!ok) break;
                 *reinterpret_cast<ChItem*>(sm + SM::ITEMS + k * sizeof(ChItem)) = im;
                 mbar_arrive(&bars[B::IF + k]);

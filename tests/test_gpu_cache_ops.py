@@ -1,6 +1,7 @@
 """jet_cache_copy and jet_cache_compact against indexing."""
 import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -104,12 +105,18 @@ def test_copy_in_a_graph_and_on_a_stream(jet):
 
 # ---------------------------------------------------------------- compaction
 def expect(table, kv, page, P):
+    out, n, to = expect_np(table.numpy(), kv, page, P)
+    return torch.from_numpy(out), n, to
+
+
+def expect_np(table, kv, page, P):
     held = sorted({int(table[s, i]) for s in range(len(kv)) for i in range(-(-kv[s] // page)) if table[s, i] >= 0})
     n = len(held)
-    holes = [i for i in range(n) if i not in set(held)]
+    kept = set(held)
+    holes = [i for i in range(n) if i not in kept]
     to = {i: i for i in held if i < n}
     to.update(zip([i for i in held if i >= n], holes))
-    out = torch.full_like(table, -1)
+    out = np.full_like(table, -1)
     for s in range(len(kv)):
         for i in range(-(-kv[s] // page)):
             if table[s, i] >= 0:
