@@ -19,6 +19,7 @@ Function names match the C entry points:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from array import array
 
@@ -51,15 +52,17 @@ class JetError(RuntimeError):
 
 
 _lib = None
+_bind = None          # the fast path of the decode step's calls (csrc/bind.cpp)
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libjet.so (raises if it has not been built)."""
-    global _lib
+    """Load libjet.so and the binding's _bind.so (raises if they have not been built)."""
+    global _lib, _bind
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
         raise ImportError(f"libjet.so not built at {path}: run linear_attention_lm_gen_b200/build.py")
+    _bind = importlib.import_module("._bind", __name__)
     _lib = declare(ctypes.CDLL(path))
     return _lib
 
@@ -114,6 +117,8 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
               "jet_gdn_range_correct", "jet_jetblock_layer", "jet_attn_rope_append", "jet_attn_paged", "jet_cache_copy",
               "jet_cache_compact", "jet_device_error"):
         getattr(L, f).restype = I
+    for f in ("jet_attn_rope_append", "jet_attn_paged", "jet_cache_copy", "jet_cache_compact"):
+        setattr(L, "at_" + f, ctypes.cast(getattr(L, f), P).value)
     return L
 
 
@@ -505,9 +510,10 @@ def jet_conv_gdn_decode_step(q, k, v, hist_in, hist_out, taps, g, beta, S, o=Non
 
 
 # ---------------------------------------------------------------- softmax attention over a paged cache
-# The decode step's calls take a few microseconds on the GPU, so their checks
-# are written to cost little: one expression per argument, the error worked out
-# only when it fails.
+# The decode step's calls take a few microseconds on the GPU. With outputs and
+# workspace given, on the current device and stream, they go through _bind,
+# which checks the arguments natively; anything else, and every error, through
+# the checks here.
 class _on:
     """Make device `index` current and issue on `stream` (default: the device's
     current stream) for the length of a call; what the call allocates belongs
@@ -631,6 +637,13 @@ def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, pag
     and page_table [nseq,max_pages] are int32 on the GPU. q_out may be q
     itself. Returns q_out [N,Hq,d]."""
     L = _lib or load_library()
+    if stream is None and q_out is not None:
+        st = _bind.rope_append(L.at_jet_attn_rope_append, q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, page_table,
+                               k_pool, v_pool, q_out, eps, interleaved)
+        if st == 0:
+            return q_out
+        if st is not None:
+            raise JetError("jet_attn_rope_append", st)
     index = _index(q, "q")
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q, k and v must be [N, heads, d]")
@@ -676,6 +689,13 @@ def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 
     max_new: the largest number of new tokens of a sequence (0: unknown); it
     only chooses the kernel. Returns o [N,Hq,d]."""
     L = _lib or load_library()
+    if stream is None and workspace is not None and o is not None:
+        st = _bind.attn_paged(L.at_jet_attn_paged, q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new, o, workspace,
+                              window, scale)
+        if st == 0:
+            return o
+        if st is not None:
+            raise JetError("jet_attn_paged", st)
     index = _index(q, "q")
     if q.dim() != 3 or not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
         raise ValueError("q must be [N, Hq, d] and the pools [pages, Hk, page, d]")
@@ -757,6 +777,12 @@ def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
     each entry dense), entry dst[i] becomes a copy of entry src[i]. src and dst
     are host lists; a destination appears once and is no source."""
     L = _lib or load_library()
+    if stream is None:
+        st = _bind.cache_copy(L.at_jet_cache_copy, pools, src, dst)
+        if st == 0:
+            return
+        if st is not None:
+            raise JetError("jet_cache_copy", st)
     base, size, step, n_pools, n_entries, index = _entries(pools)
     a, b = _host_ints(src, "src"), _host_ints(dst, "dst")
     if len(a) != len(b):
@@ -779,6 +805,13 @@ def jet_cache_compact(pools, page_table, kv_lens, page_size: int, page_table_out
     (page_table_out, n_live [1]): the rewritten tables (page_table itself may
     be given) and the number of live pages, on the GPU."""
     L = _lib or load_library()
+    if stream is None and workspace is not None:
+        st = _bind.cache_compact(L.at_jet_cache_compact, pools, page_table, kv_lens, page_size, page_table_out, n_live,
+                                 workspace)
+        if st == 0:
+            return page_table_out, n_live
+        if st is not None:
+            raise JetError("jet_cache_compact", st)
     base, size, step, n_pools, n_pages, index = _entries(pools)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [nseq, max_pages]")

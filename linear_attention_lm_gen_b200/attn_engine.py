@@ -227,10 +227,11 @@ class JetAttnEngine:
             raise ValueError(f"the batch has {batch.tokens} new tokens, q has {q.shape[0]}")
         gq, gk = self.gammas[layer]
         kp, vp = self.k[layer], self.v[layer]
-        y = jet_attn_rope_append(q, k, v, gq, gk, self.inv_freq, batch.cu_q, batch.kv_lens, batch.page_table, kp, vp,
+        y = torch.empty((batch.tokens, self.Hq, self.d), device=self.device, dtype=self.dtype)
+        y = jet_attn_rope_append(q, k, v, gq, gk, self.inv_freq, batch.cu_q, batch.kv_lens, batch.page_table, kp, vp, y,
                                  eps=self.eps, interleaved=self.interleaved)
         need = jet_attn_paged_workspace_size(len(batch.seqs), batch.tokens, self.Hq, self.Hk, self.d, self.dtype)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, device=self.device, dtype=torch.uint8)
-        return jet_attn_paged(y, kp, vp, batch.cu_q, batch.kv_lens, batch.page_table, max(batch.new), None, self._ws,
-                              window=self.windows[layer], scale=self.scale)
+        return jet_attn_paged(y, kp, vp, batch.cu_q, batch.kv_lens, batch.page_table, max(batch.new),
+                              torch.empty_like(y), self._ws, window=self.windows[layer], scale=self.scale)

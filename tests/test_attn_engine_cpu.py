@@ -19,7 +19,7 @@ def fake_copy(pools, src, dst):
         p[dst] = p[src].clone()
 
 
-def fake_append(q, k, v, gq, gk, inv_freq, cu, lens, table, kp, vp, *, eps, interleaved):
+def fake_append(q, k, v, gq, gk, inv_freq, cu, lens, table, kp, vp, q_out, *, eps, interleaved):
     """Writes the tokens' values at their positions (no norm, no rotation)."""
     for s in range(len(lens)):
         n = int(cu[s + 1] - cu[s])
