@@ -91,7 +91,7 @@ attn::Work make_work(const attn::Cache& c, const attn::Batch& b, int Hk, int G, 
 
 template <typename T, int RW, int PB, int BLOCKS>
 jet_status launch_join(const attn::Work& w, const attn::Slots& sl, void* o, int d, int n_cta, cudaStream_t s) {
-    static_assert(3 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
+    static_assert(4 * kMaxSMs <= attn::MAX_PARTS, "an item's parts");
     const int per = attn::JOIN_WARPS * RW;
     const dim3 grid(n_cta - 1, (sl.rows + per - 1) / per);
     return launch(attn::attn_join_kernel<T, RW, PB, BLOCKS>, grid, dim3(attn::JOIN_WARPS * 32), 0, s, sl, (T*)o, w.Hk * w.G,
@@ -114,13 +114,16 @@ jet_status launch_attn_decode(const void* q, int64_t q_stride, const attn::Cache
     return st != JET_OK ? st : launch_join<__nv_bfloat16, 1, 16, 2>(w, sl, o, d, n_cta, s);
 }
 
+template <int DP>
 jet_status launch_attn_f32(const void* q, int64_t q_stride, const attn::Cache& c, const attn::Batch& b, void* o, void* ws,
                            int Hk, int G, int d, int window, float scale, cudaStream_t s) {
-    const int n_cta = launch_sms() * attn::F32_CTAS;
-    const attn::Work w = make_work(c, b, Hk, G, window, attn::F32_ROWS, attn::F32_KT, 96, 192);
+    typedef attn::F32Cfg<DP> C;
+    const int n_cta = launch_sms() * C::CTAS;
+    const attn::Work w = make_work(c, b, Hk, G, window, attn::F32_ROWS, attn::F32_KT, 96, 128);
     const attn::Slots sl = make_slots(ws, n_cta, attn::F32_ROWS, d);
-    if (smem_attr(attn::attn_f32_kernel, attn::F32_SMEM) != JET_OK) return JET_ERR_CUDA;
-    const jet_status st = launch(attn::attn_f32_kernel, dim3(n_cta), dim3(attn::F32_THREADS), attn::F32_SMEM, s,
+    auto kern = attn::attn_f32_kernel<DP>;
+    if (smem_attr(kern, C::SMEM) != JET_OK) return JET_ERR_CUDA;
+    const jet_status st = launch(kern, dim3(n_cta), dim3(attn::F32_THREADS), C::SMEM, s,
                                  (const float*)q, (long long)q_stride, w, sl, (float*)o, d, scale * 1.44269504f);
     return st != JET_OK ? st : launch_join<float, 1, 16, 2>(w, sl, o, d, n_cta, s);
 }
@@ -236,7 +239,8 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
 
 size_t jet_attn_paged_workspace_size(int nseq, int N, int Hq, int Hk, int d, jet_dtype dt) {
     if (check_attn_shape(AttnShape{nseq, N, 1, 1, 16, Hq, Hk, d, dt}) != JET_OK) return 0;
-    if (dt == JET_F32) return slot_layout(kMaxSMs * attn::F32_CTAS, attn::F32_ROWS, d).bytes;
+    if (dt == JET_F32)
+        return slot_layout(kMaxSMs * (d <= 64 ? attn::F32Cfg<64>::CTAS : attn::F32Cfg<128>::CTAS), attn::F32_ROWS, d).bytes;
     const int per_sm = d <= 64 ? attn::DecCfg<64>::CTAS : attn::DecCfg<128>::CTAS;
     return std::max(slot_layout(kMaxSMs * per_sm, attn::DEC_ROWS, d).bytes,
                     slot_layout(kMaxSMs, chunk_rows(Hq / Hk), d).bytes);
@@ -270,7 +274,9 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
                         page_shift_of(page_size)};
     const attn::Batch b{cu_q, kv_lens, nseq, N};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dt == JET_F32) return launch_attn_f32(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
+    if (dt == JET_F32)
+        return d <= 64 ? launch_attn_f32<64>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
+                       : launch_attn_f32<128>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
     const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;
     if (typical * (Hq / Hk) > kDecodeRows)
         return d <= 64 ? launch_attn_chunk<1>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)

@@ -11,6 +11,8 @@
 // until the item ends, when the four are joined through shared memory. A
 // stage lies in one page, so each costs a warp one page-table entry, read a
 // step ahead. Work is divided as k_attn_sched.cuh says: two CTAs to an SM.
+// 256 sequences of up to 8192 positions (1.04 GB): 169 us, 6.2 TB/s, 94% of the
+// copy rate; one CTA with six stages 225 us, three with two stages 168 us.
 //
 // Positions outside the item's range are filled with zeros, never read. The
 // weights are rounded to bf16 for the second product (the type the tensor

@@ -4,11 +4,12 @@
 // share it); a step is 64 positions, copied asynchronously into padded rows
 // of shared memory: the next K while the values are summed, the next V while
 // the next scores are computed. A thread computes 4 x 4 scores and holds 4
-// rows x 8 columns of the result; a row's 16 threads are half a warp, so the
+// rows x 4 or 8 columns of the result; a row's 16 threads are half a warp, so the
 // running maximum and sum need four shuffles. A product is 64 fused
 // multiply-adds for every 8 loads of 16 bytes, which broadcast within a warp:
-// bound by the multiply-adds. Work is divided as k_attn_sched.cuh says, two
-// CTAs to an SM.
+// bound by the multiply-adds (0.35 of their rate over 3 sequences of 100 to 333
+// new tokens, 39 us; as packed pairs 43 us). Work is divided as k_attn_sched.cuh says, four
+// CTAs to an SM for d <= 64 and two above.
 //
 // Positions outside the item's range are zero-filled, never read. A masked
 // weight is stored as -1 and left out of the sum by a test (only in steps
@@ -20,13 +21,19 @@
 namespace jet {
 namespace attn {
 
-constexpr int F32_ROWS = 32, F32_KT = 64, F32_THREADS = 128, F32_CTAS = 2;
-constexpr int F32_LD = 128 + 4, F32_PLD = F32_KT + 4;
-constexpr int F32_SMEM = 4 * (F32_ROWS * F32_LD + 2 * F32_KT * F32_LD + F32_ROWS * F32_PLD) + 8 * 2 * F32_KT;
+constexpr int F32_ROWS = 32, F32_KT = 64, F32_THREADS = 128;
 
-__global__ void __launch_bounds__(F32_THREADS, F32_CTAS)
+template <int DP> struct F32Cfg {                       // DP: d rounded up to 64 or 128
+    static constexpr int CTAS = DP == 64 ? 4 : 2;       // per SM
+    static constexpr int LD = DP + 4, PLD = F32_KT + 4;
+    static constexpr int SMEM = 4 * (F32_ROWS * LD + 2 * F32_KT * LD + F32_ROWS * PLD) + 8 * 2 * F32_KT;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(F32_THREADS, F32Cfg<DP>::CTAS)
 attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots sl, float* __restrict__ o, int d,
                 float scale2) {
+    constexpr int F32_LD = F32Cfg<DP>::LD, F32_PLD = F32Cfg<DP>::PLD, NC = DP / 64, CH = DP / 4;
     extern __shared__ __align__(128) float sf[];
     float* Q = sf;
     float* K = Q + F32_ROWS * F32_LD;
@@ -77,8 +84,8 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
         };
         auto fetch = [&](const float* src, float* to, int step) {      // one copy group, by all threads
             if (step < b1)
-                for (int e = tid; e < F32_KT * 32; e += F32_THREADS) {
-                    const int row = e >> 5, ch = e & 31;
+                for (int e = tid; e < F32_KT * CH; e += F32_THREADS) {
+                    const int row = e / CH, ch = e % CH;
                     if (ch >= per) continue;
                     const long long off = offs[(step & 1) * F32_KT + row];
                     cp16(dec_smem(to + row * F32_LD + ch * 4), src + (off < 0 ? 0 : off + ch * 4), off >= 0);
@@ -86,8 +93,8 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
             cp_commit();
         };
         find(b0);
-        for (int e = tid; e < F32_ROWS * 32; e += F32_THREADS) {
-            const int row = e >> 5, ch = e & 31, tok = row / w.gt, hd = row - tok * w.gt;
+        for (int e = tid; e < F32_ROWS * CH; e += F32_THREADS) {
+            const int row = e / CH, ch = e % CH, tok = row / w.gt, hd = row - tok * w.gt;
             if (ch >= per) continue;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (tok < it.nt && it.hh % w.hs * w.gt + hd < w.G)
@@ -96,14 +103,14 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
             *reinterpret_cast<float4*>(Q + row * F32_LD + ch * 4) = v;
         }
         int pos[4];
-        float m[4], l[4], acc[4][8];
+        float m[4], l[4], acc[4][4 * NC];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             pos[i] = it.p_first + min((rt * 4 + i) / w.gt, it.nt - 1);
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
+            for (int c = 0; c < 4 * NC; ++c) acc[i][c] = 0.f;
         }
         __syncthreads();
         fetch(kp, K, b0);
@@ -155,7 +162,7 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
                 }
                 l[i] = l[i] * f + sum;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) acc[i][c] *= f;
+                for (int c = 0; c < 4 * NC; ++c) acc[i][c] *= f;
             }
             __syncthreads();                            // K is done, P is there
             fetch(kp, K, step + 1);
@@ -168,15 +175,21 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
                 for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4*>(P + (rt * 4 + i) * F32_PLD + j);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    const float4 v0 = *reinterpret_cast<const float4*>(V + (j + jj) * F32_LD + kt * 4);
-                    const float4 v1 = *reinterpret_cast<const float4*>(V + (j + jj) * F32_LD + 64 + kt * 4);
-                    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    float v[4 * NC];
+#pragma unroll
+                    for (int h = 0; h < NC; ++h) {
+                        const float4 x = *reinterpret_cast<const float4*>(V + (j + jj) * F32_LD + h * 64 + kt * 4);
+                        v[4 * h] = x.x;
+                        v[4 * h + 1] = x.y;
+                        v[4 * h + 2] = x.z;
+                        v[4 * h + 3] = x.w;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float p = jj == 0 ? p4[i].x : jj == 1 ? p4[i].y : jj == 2 ? p4[i].z : p4[i].w;
                         if (!partial || !(p < 0.f)) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) acc[i][c] = fmaf(p, v[c], acc[i][c]);
+                            for (int c = 0; c < 4 * NC; ++c) acc[i][c] = fmaf(p, v[c], acc[i][c]);
                         }
                     }
                 }
@@ -197,7 +210,7 @@ attn_f32_kernel(const float* __restrict__ q, long long q_stride, Work w, Slots s
             float* to = slot < 0 ? o + dst : sl.o + ((long long)slot * sl.rows + r) * d;
             const float f = slot < 0 ? inv : 1.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < NC; ++h)
                 if (h * 64 + kt * 4 < d)
                     *reinterpret_cast<float4*>(to + h * 64 + kt * 4) =
                         make_float4(acc[i][h * 4] * f, acc[i][h * 4 + 1] * f, acc[i][h * 4 + 2] * f, acc[i][h * 4 + 3] * f);
