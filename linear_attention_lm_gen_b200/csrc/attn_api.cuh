@@ -308,11 +308,11 @@ jet_status make_pools(cache::Pools& P, void* const* pools, const int64_t* entry_
     return JET_OK;
 }
 
-// blocks for n entries of every pool: one piece each, at most eight blocks to an SM
-unsigned copy_grid(const cache::Pools& P, long long n) {
+// blocks for n entries of every pool: one piece each, up to a limit
+unsigned copy_grid(const cache::Pools& P, long long n, long long limit) {
     long long pieces = 0;
     for (int i = 0; i < P.n; ++i) pieces += (P.bytes[i] + cache::PIECE - 1) / cache::PIECE * n;
-    return (unsigned)std::max<long long>(1, std::min<long long>(pieces, 8 * kMaxSMs));
+    return (unsigned)std::max<long long>(1, std::min(pieces, limit));
 }
 
 // Every index in range, every destination once and none also a source. One
@@ -349,7 +349,7 @@ template <int CAP>
 jet_status launch_copy(const cache::Pools& P, const int* src, const int* dst, int n, cudaStream_t s) {
     cache::Pairs<CAP> pairs;
     for (int i = 0; i < n; ++i) pairs.e[i] = make_int2(src[i], dst[i]);
-    return launch(cache::copy_kernel<CAP>, dim3(copy_grid(P, n)), dim3(cache::THREADS), 0, s, P, pairs, n);
+    return launch(cache::copy_kernel<CAP>, dim3(copy_grid(P, n, 1 << 16)), dim3(cache::THREADS), 0, s, P, pairs, n);
 }
 
 constexpr int kFewPairs = 256, kManyPairs = 3584;     // 2 KB and 28 KB of kernel parameters
@@ -419,8 +419,9 @@ jet_status jet_cache_compact(void* const* pools, const int64_t* entry_bytes, con
     st = launch(cache::compact_plan_kernel, dim3(1), dim3(cache::PLAN_THREADS), smem, s, page_table, kv_lens, nseq,
                 max_pages, shift, n_pages, plan, n_live);
     if (st != JET_OK) return st;
-    // the number of moves is known on the device only: at most half the pages
-    return launch(cache::compact_move_kernel, dim3(copy_grid(P, std::max(1, n_pages / 2))), dim3(cache::THREADS), 0, s,
+    // the number of moves is known on the device only: at most half the pages. 16 blocks to an SM, twice what fits at
+    // once: 8192 pages half live 186 -> 177 us against 8, and 239 us with a block for every piece there could be
+    return launch(cache::compact_move_kernel, dim3(copy_grid(P, std::max(1, n_pages / 2), 16 * kMaxSMs)), dim3(cache::THREADS), 0, s,
                   P, page_table, page_table_out, kv_lens, nseq, max_pages, shift, n_pages, (const int*)n_live, plan);
 }
 
