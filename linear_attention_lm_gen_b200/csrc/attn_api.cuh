@@ -178,8 +178,22 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
     return st != JET_OK ? st : launch_join<__nv_bfloat16, 4, 2, 4>(w, sl, o, d, n_cta, s);
 }
 
-// rows per sequence and cache head up to which the decode kernel is taken
-constexpr int kDecodeRows = 16;
+// The decode kernel is taken where a sequence's rows fit one of its tiles (one
+// read of the cache): 256 sequences of one token 169 us against 209 with the
+// chunk kernel. It is also taken where there is little to do at all, since it
+// starts sooner: its tiles read the cache again for every 16 rows, so its time
+// grows with rows times positions (bounded here by the tables' width or the
+// window), and the two are level at about 1.5 million of them, 192 added for
+// an item's ends (12 heads over 2; us, decode against chunk kernel: 128 tokens
+// over 500 19 / 23, 8 x 8 over 500 16 / 21, 8 x 32 over nothing 11 / 13;
+// 8 x 32 over 500 25 / 24, 64 over 3000 26 / 24, 8 x 128 over nothing 28 / 14).
+constexpr double kDecodeWork = 1.5e6;
+bool take_decode(int nseq, int N, int max_new, long long table_positions, int Hq, int G, int window) {
+    const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;
+    if (typical * G <= attn::DEC_ROWS) return true;
+    const double seen = window > 0 ? std::min<double>((double)table_positions, (double)window + typical) : (double)table_positions;
+    return (double)N * Hq * (seen + 192.0) <= kDecodeWork;
+}
 
 }  // namespace
 
@@ -277,8 +291,7 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
     if (dt == JET_F32)
         return d <= 64 ? launch_attn_f32<64>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
                        : launch_attn_f32<128>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
-    const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;
-    if (typical * (Hq / Hk) > kDecodeRows)
+    if (!take_decode(nseq, N, max_new, (long long)max_pages * page_size, Hq, Hq / Hk, window))
         return d <= 64 ? launch_attn_chunk<1>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)
                        : launch_attn_chunk<2>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s);
     return d <= 64 ? launch_attn_decode<64>(q, q_stride, c, b, o, workspace, Hk, Hq / Hk, d, window, scale, s)

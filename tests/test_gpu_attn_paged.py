@@ -19,9 +19,29 @@ def jet():
     return m
 
 
+WIDE = False
+
+
+@pytest.fixture(autouse=True, params=["narrow", "wide"])
+def _tables(request):
+    """Every test with the tables as narrow as they can be and with wide ones: the tables bound the lengths that the
+    host knows of, and batches that can only be small take the decode kernel whatever their rows."""
+    global WIDE
+    WIDE = request.param == "wide"
+
+
+def table_of(b):
+    if not WIDE:
+        return b.table
+    cols = int(1.6e6 / (b.N * b.Hq)) // b.page + b.table.shape[1]
+    t = torch.full((b.table.shape[0], cols), -1, dtype=torch.int32, device=b.device)
+    t[:, :b.table.shape[1]] = b.table
+    return t
+
+
 def call(jet, b, max_new=None, **kw):
     o = torch.full((b.N, b.Hq, b.d), 7.0, device=b.device, dtype=b.dtype)
-    jet.jet_attn_paged(b.q, b.k_pool, b.v_pool, b.cu, b.kv_lens, b.table, max(b.new) if max_new is None else max_new,
+    jet.jet_attn_paged(b.q, b.k_pool, b.v_pool, b.cu, b.kv_lens, table_of(b), max(b.new) if max_new is None else max_new,
                        o, **kw)
     return o
 
@@ -235,7 +255,9 @@ def test_queries_with_a_token_stride_and_an_own_stream(jet):
     wide[:, :12] = b.q
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    o = jet.jet_attn_paged(wide[:, :12], b.k_pool, b.v_pool, b.cu, b.kv_lens, b.table, 300, stream=side)
+    t = table_of(b)
+    side.wait_stream(torch.cuda.current_stream())
+    o = jet.jet_attn_paged(wide[:, :12], b.k_pool, b.v_pool, b.cu, b.kv_lens, t, 300, stream=side)
     side.synchronize()
     assert torch.equal(o, ref)
 
@@ -256,7 +278,8 @@ def test_a_captured_graph_follows_new_lengths(jet, max_new, new):
     b = Batch(new, [500, 300, 20], Hq=12, Hk=2, d=128, page=64, seed=18)
     ws = torch.empty(max(16, jet.jet_attn_paged_workspace_size(3, b.N, 12, 2, 128)), device="cuda", dtype=torch.uint8)
     o = torch.empty((b.N, 12, 128), device="cuda", dtype=BF)
-    run = lambda: jet.jet_attn_paged(b.q, b.k_pool, b.v_pool, b.cu, b.kv_lens, b.table, max_new, o, ws)
+    t = table_of(b)
+    run = lambda: jet.jet_attn_paged(b.q, b.k_pool, b.v_pool, b.cu, b.kv_lens, t, max_new, o, ws)
     run()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -283,7 +306,7 @@ def test_bad_device_data_is_flagged_and_reads_nothing(jet, dtype, max_new):
             b.table[1, 1] = b.n_pages
             b.table[1, 2] = -5
         elif what == "length":
-            b.kv_lens[1] = 16 * b.table.shape[1] + 1
+            b.kv_lens[1] = 2 ** 30 + 1              # no table holds that many
         else:
             b.cu[2] = b.N + 5
         o = call(jet, b, max_new=max_new)
