@@ -24,7 +24,11 @@ All layers share the page numbering: page i is entry i of every layer's pools.
 If every layer has a window, pages that lie before all windows are given up as
 the sequences advance. The host keeps the page tables and reference counts;
 each step sends its tables to the GPU in one copy. Everything is issued on
-torch's current stream.
+torch's current stream. Steps on two streams share no scratch memory, but the
+pages: a step that gives pages up or takes them has to be ordered with the
+others, as with any tensor. Between a step's begin and its last attend, do not
+fork or release its sequences; a batch from before a compact() is refused,
+since its pages have moved.
 """
 from __future__ import annotations
 
@@ -45,6 +49,7 @@ class AttnBatch:
     cu_q: torch.Tensor     # [n + 1] int32
     kv_lens: torch.Tensor  # [n] int32, the new tokens included
     page_table: torch.Tensor   # [n, width] int32
+    epoch: int             # compactions before it
 
     @property
     def tokens(self) -> int:
@@ -77,7 +82,7 @@ class JetAttnEngine:
         self.row: dict = {}                                 # sequence id -> row of the tables
         self.len: dict = {}                                 # sequence id -> positions in the cache
         self._first: dict = {}                              # sequence id -> first page still held
-        self._ws = None
+        self._epoch = 0                                     # compactions so far
 
     # ---------------------------------------------------------------- sequences and pages
     @property
@@ -162,6 +167,7 @@ class JetAttnEngine:
         out, live = None, None
         for i in range(0, len(pools), 64):                  # the plan depends on the tables alone
             out, live = jet_cache_compact(pools[i:i + 64], table, lens, self.page)
+        self._epoch += 1
         self._table[rows] = out.cpu().numpy()
         n = int(live.item())
         self._ref[:] = 0
@@ -217,7 +223,7 @@ class JetAttnEngine:
         host[2 * n + 1:] = self._table[[self.row[s] for s in seqs], :width].ravel()
         dev = torch.from_numpy(host).to(self.device, non_blocking=True)
         return AttnBatch(seqs, [int(new[s]) for s in seqs], dev[:n + 1], dev[n + 1:2 * n + 1],
-                         dev[2 * n + 1:].view(n, width))
+                         dev[2 * n + 1:].view(n, width), self._epoch)
 
     def attend(self, layer: int, batch: AttnBatch, q, k, v) -> torch.Tensor:
         """One layer of a step: q [N,Hq,d], k, v [N,Hk,d] of the batch's new
@@ -225,13 +231,15 @@ class JetAttnEngine:
         values enter the cache; returns o [N,Hq,d]."""
         if q.shape[0] != batch.tokens:
             raise ValueError(f"the batch has {batch.tokens} new tokens, q has {q.shape[0]}")
+        if batch.epoch != self._epoch:
+            raise ValueError("the batch is from before a compaction: its pages have moved")
         gq, gk = self.gammas[layer]
         kp, vp = self.k[layer], self.v[layer]
         y = torch.empty((batch.tokens, self.Hq, self.d), device=self.device, dtype=self.dtype)
         y = jet_attn_rope_append(q, k, v, gq, gk, self.inv_freq, batch.cu_q, batch.kv_lens, batch.page_table, kp, vp, y,
                                  eps=self.eps, interleaved=self.interleaved)
         need = jet_attn_paged_workspace_size(len(batch.seqs), batch.tokens, self.Hq, self.Hk, self.d, self.dtype)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, device=self.device, dtype=torch.uint8)
+        # of its own: a batch on another stream, or another captured graph, has another one
+        ws = torch.empty(need, device=self.device, dtype=torch.uint8)
         return jet_attn_paged(y, kp, vp, batch.cu_q, batch.kv_lens, batch.page_table, max(batch.new),
-                              torch.empty_like(y), self._ws, window=self.windows[layer], scale=self.scale)
+                              torch.empty_like(y), ws, window=self.windows[layer], scale=self.scale)

@@ -260,6 +260,33 @@ def test_checks_come_before_changes(make):
         ae.JetAttnEngine(2, 2, 1, 8, 4, windows=[1], device="cpu")
 
 
+def test_a_batch_from_before_a_compaction_is_refused(make):
+    """Its table names pages that have moved."""
+    e = make()
+    t = Texts(e)
+    for s in "ab":
+        e.admit(s)
+        t.step({s: 20})
+    t.release("a")
+    b = e.begin({"b": 1})
+    e.compact()
+    x = torch.zeros(1, 1, 8)
+    with pytest.raises(ValueError, match="compaction"):
+        e.attend(0, b, torch.zeros(1, 2, 8), x, x)
+
+
+def test_batches_do_not_share_a_workspace(make, monkeypatch):
+    """Two steps may be on different streams, or in two captured graphs."""
+    held = []
+    monkeypatch.setattr(ae, "jet_attn_paged", lambda *a, **kw: held.append(a[8]))
+    e = make()
+    x = torch.zeros(1, 1, 8)
+    for s in "ab":
+        e.admit(s)
+        e.attend(0, e.begin({s: 1}), torch.zeros(1, 2, 8), x, x)
+    assert held[0].data_ptr() != held[1].data_ptr()
+
+
 def test_state_engine_forks(monkeypatch):
     monkeypatch.setattr(eng, "jet_cache_copy", fake_copy)
     e = eng.JetEngine(torch.zeros(64, 32), torch.zeros(32, 8), 2, 16, 32, max_seqs=4, chunk_tokens=16)
