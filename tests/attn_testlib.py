@@ -2,6 +2,7 @@
 paged batches with poisoned unused memory, and the formulas in 64 bits."""
 from __future__ import annotations
 
+import ctypes
 import random
 
 import torch
@@ -119,3 +120,37 @@ def check_attention(got, b, window=0, scale=None):
     assert torch.isfinite(got).all(), "non-finite outputs"
     bad = ((got - o).abs() - attention_bound(o, a, b.dtype)).amax().item() if o.numel() else 0.0
     assert bad <= 0.0, f"error above its bound by {bad:.3e}; largest error {(got - o).abs().amax().item():.3e}"
+
+
+class _KernelNode(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("dims", ctypes.c_uint * 7), ("params", ctypes.c_void_p),
+                ("extra", ctypes.c_void_p), ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def launched(run):
+    """Names (mangled) of the kernels that run() launches: captured into a graph, whose nodes are looked at; not replayed."""
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        run()
+    cu = ctypes.CDLL("libcuda.so.1")
+    P, graph = ctypes.c_void_p, ctypes.c_void_p(g.raw_cuda_graph())
+
+    def ok(status):
+        assert status == 0, f"driver call returned {status}"
+    n = ctypes.c_size_t()
+    ok(cu.cuGraphGetNodes(graph, None, ctypes.byref(n)))
+    nodes = (P * n.value)()
+    ok(cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)))
+    names = []
+    for node in nodes:
+        kind = ctypes.c_int()
+        ok(cu.cuGraphNodeGetType(P(node), ctypes.byref(kind)))
+        if kind.value == 0:                    # a kernel
+            p, name = _KernelNode(), ctypes.c_char_p()
+            ok(cu.cuGraphKernelNodeGetParams_v2(P(node), ctypes.byref(p)))
+            ok(cu.cuFuncGetName(ctypes.byref(name), P(p.func)) if p.func
+               else cu.cuKernelGetName(ctypes.byref(name), P(p.kern)))
+            names.append(name.value.decode())
+    return names
