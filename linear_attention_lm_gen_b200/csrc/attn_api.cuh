@@ -366,7 +366,8 @@ jet_status launch_copy(const cache::Pools& P, const int* src, const int* dst, in
 }
 
 constexpr int kFewPairs = 256, kManyPairs = 3584;     // 2 KB and 28 KB of kernel parameters
-constexpr int kMaxCompactPages = 1 << 20;             // the plan's bitmap: 128 KB of shared memory
+constexpr int kMaxCompactPages = 1 << 20;
+constexpr size_t kPlanSmemMax = kMaxCompactPages / 8; // the plan's bitmap: 128 KB of shared memory
 
 }  // namespace
 
@@ -428,7 +429,9 @@ jet_status jet_cache_compact(void* const* pools, const int64_t* entry_bytes, con
                               reinterpret_cast<int*>(w + 256 + moves_bytes)};
     const int shift = page_shift_of(page_size);
     const size_t smem = sizeof(uint32_t) * (((size_t)n_pages + 31) / 32);
-    if (smem_attr(cache::compact_plan_kernel, smem) != JET_OK) return JET_ERR_CUDA;
+    // The kernel's own variables count against the 48 KB that need no opt-in, so it is asked for from 32 KB on, and
+    // always for the largest bitmap: a smaller call on another thread cannot lower it before this one's launch.
+    if (smem > 32 * 1024 && smem_attr(cache::compact_plan_kernel, kPlanSmemMax) != JET_OK) return JET_ERR_CUDA;
     st = launch(cache::compact_plan_kernel, dim3(1), dim3(cache::PLAN_THREADS), smem, s, page_table, kv_lens, nseq,
                 max_pages, shift, n_pages, plan, n_live);
     if (st != JET_OK) return st;
