@@ -27,7 +27,8 @@ each step sends its tables to the GPU in one copy. Everything is issued on
 torch's current stream. Steps on two streams share no scratch memory, but the
 pages: a step that gives pages up or takes them has to be ordered with the
 others, as with any tensor. Between a step's begin and its last attend, do not
-fork or release its sequences; a batch from before a compact() is refused,
+fork or release its sequences, nor begin another step of them, not even one
+that is refused for want of room; a batch from before a compact() is refused,
 since its pages have moved.
 """
 from __future__ import annotations
@@ -179,34 +180,30 @@ class JetAttnEngine:
     # ---------------------------------------------------------------- steps
     def begin(self, new: dict) -> AttnBatch:
         """Room for new[seq] >= 1 new tokens of each sequence, in the order of
-        `new`. Every check comes before any page is taken."""
+        `new`. The checks come before any change. Pages that no window of
+        these sequences will see again are then given up, which makes room;
+        if there is still too little, no page is taken (RuntimeError)."""
         seqs = list(new)
         self._known(seqs)
         if not seqs or any(int(n) < 1 for n in new.values()):
             raise ValueError("a step needs at least one new token of each of its sequences")
-        keep = max(self.windows) if all(self.windows) else 0
-        need, spare = 0, 0
+        need = 0
         for s in seqs:
             total = self.len[s] + new[s]
             if -(-total // self.page) > self._table.shape[1]:
                 raise ValueError(f"sequence {s!r} would outgrow the cache's longest sequence")
             need += -(-total // self.page) - -(-self.len[s] // self.page)
-        # pages before every window of the step's tokens
-        gone = {}
-        if keep:
+        keep = max(self.windows) if all(self.windows) else 0
+        if keep:                                            # pages before every window of the step's tokens
             for s in seqs:
                 f = max(0, self.len[s] - keep + 1) // self.page
-                t = self._table[self.row[s]][self._first[s]:f]
-                gone[s] = f
-                spare += int((self._ref[t[t >= 0]] == 1).sum())
-        if need > len(self._free) + spare:
+                if f > self._first[s]:
+                    t = self._table[self.row[s]][self._first[s]:f]
+                    self._drop(t[t >= 0])
+                    t.fill(-1)
+                    self._first[s] = f
+        if need > len(self._free):
             raise RuntimeError("page cache is full")
-        for s, f in gone.items():
-            if f > self._first[s]:
-                t = self._table[self.row[s]][self._first[s]:f]
-                self._drop(t[t >= 0])
-                t.fill(-1)
-                self._first[s] = f
         for s in seqs:
             t = self._table[self.row[s]]
             for i in range(-(-self.len[s] // self.page), -(-(self.len[s] + new[s]) // self.page)):
