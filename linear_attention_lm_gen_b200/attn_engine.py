@@ -136,24 +136,22 @@ class JetAttnEngine:
         if tail and len(children) > len(self._free):
             raise RuntimeError("page cache is full")
         t = self._table[self.row[parent]]
+        # the copies first: if one fails, nothing has changed but free pages
+        dst = heapq.nsmallest(len(children), self._free) if tail else []
+        if dst:
+            pools = self.pools
+            for i in range(0, len(pools), 64):              # pools per call
+                jet_cache_copy(pools[i:i + 64], [int(t[n])] * len(dst), dst)
         shared = t[:n][t[:n] >= 0]
-        src, dst = [], []
         for c in children:
             self.admit(c)
             tc = self._table[self.row[c]]
             tc[:n] = t[:n]
             self._ref[shared] += 1
             if tail:
-                p = heapq.heappop(self._free)
-                self._ref[p] = 1
-                tc[n] = p
-                src.append(int(t[n]))
-                dst.append(p)
+                tc[n] = heapq.heappop(self._free)           # as in dst
+                self._ref[tc[n]] = 1
             self.len[c], self._first[c] = self.len[parent], self._first[parent]
-        if dst:
-            pools = self.pools
-            for i in range(0, len(pools), 64):              # pools per call
-                jet_cache_copy(pools[i:i + 64], src, dst)
 
     def compact(self) -> int:
         """Move the live pages to the lowest entries of the pools; returns

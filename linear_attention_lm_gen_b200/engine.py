@@ -91,10 +91,10 @@ class JetEngine:
             raise KeyError("a child is already admitted or appears twice")
         if len(children) > len(self._free):
             raise RuntimeError("state cache is full")
-        dst = [self._free.pop() for _ in children]
+        dst = self._free[::-1][:len(children)]             # the entries that pop() will hand out
         jet_cache_copy([self.S, self.hist], [self.slot[seq]] * len(dst), dst)
-        for c, s in zip(children, dst):
-            self.slot[c] = s
+        for c in children:
+            self.slot[c] = self._free.pop()
             self.pos[c] = self.pos[seq]
 
     def release(self, seq) -> None:
