@@ -242,6 +242,7 @@ append_kernel(AppendArgs a, Cache c, Batch b) {
                             unpair(f[j][i + 1], lo, hi);
                             pb = pair(hi, lo);
                         }
+                        if (!rotated) pa = pb = 0;          // no partner: zero times a non-finite one would not be zero
                         y[j][i] = fma2(f[j][i], co.x, mul2(pa, cp.x));
                         y[j][i + 1] = fma2(f[j][i + 1], co.y, mul2(pb, cp.y));
                     }
