@@ -161,6 +161,10 @@ struct ChItem {
 };
 constexpr int CH_QUEUE = 4;
 constexpr int CH_READERS = 11;      // warps that read the queue: softmax, products, loads, V
+// Arrivals that free a stage of the ring: its products' completion, and warp
+// 10's once it has seen the stage. Its waits tell phases apart by parity only,
+// so the ring must not run two phases ahead of it.
+constexpr int CH_RELEASES = 2;
 
 #ifdef JET_TEST_WAIT_EXPIRY
 // test builds only: leave out the first scores of tile A, so that the wait for them runs out
@@ -187,7 +191,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
     if (tid == 0) {
         for (int i = 0; i < B::N; ++i)
-            mbar_init(&bars[i], i >= B::P && i < B::P + 2 ? 4 : i >= B::IE && i < B::IE + 4 ? CH_READERS : 1);
+            mbar_init(&bars[i], i >= B::EMPTY && i < B::EMPTY + ST ? CH_RELEASES
+                                : i >= B::P && i < B::P + 2        ? 4
+                                : i >= B::IE && i < B::IE + 4      ? CH_READERS
+                                                                   : 1);
         *abort_flag = 0;
         *odd_flag = 0;
         fence_mbar_init();
@@ -573,7 +580,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                      wait_for(&bars[B::FULL + slot], (vi / ST) & 1, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (!im.partial(step)) continue;
+                if (lane == 0) mbar_arrive(&bars[B::EMPTY + kv % ST]);
+                if (!im.partial(step)) {
+                    if (lane == 0) mbar_arrive(&bars[B::EMPTY + slot]);
+                    continue;
+                }
                 const int k0 = im.lo + step * CH_KT;
                 uint8_t* V = sm + SM::KV + slot * SM::TILE;
                 // rows outside the range to zero
@@ -607,7 +618,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 __threadfence_block();
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B::FIX + slot]);
+                if (lane == 0) {
+                    mbar_arrive(&bars[B::FIX + slot]);
+                    mbar_arrive(&bars[B::EMPTY + slot]);
+                }
             }
         }
         if (!ok) *abort_flag = 1;
