@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import importlib
 import os
+import warnings
 from array import array
 
 import torch
@@ -52,17 +53,33 @@ class JetError(RuntimeError):
 
 
 _lib = None
-_bind = None          # the fast path of the decode step's calls (csrc/bind.cpp)
+_bind = None          # the fast path of the decode step's calls (csrc/bind.cpp); without it the checks here do
+
+
+def _load_bind():
+    """The module _bind, or None, with a warning, if it is missing or was built for another torch or Python."""
+    from .build import bind_abi
+    try:
+        m = importlib.import_module("._bind", __name__)
+        found, abi = getattr(m, "abi", "an unknown one"), bind_abi()
+        if found == abi:
+            return m
+        why = f"it was built for {found}, this is {abi}"
+    except ImportError as e:
+        why = str(e)
+    warnings.warn(f"_bind.so cannot be used ({why}): attention and cache calls take longer on the host; "
+                  "run linear_attention_lm_gen_b200/build.py", RuntimeWarning, stacklevel=3)
+    return None
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libjet.so and the binding's _bind.so (raises if they have not been built)."""
+    """Load libjet.so (raises if it has not been built) and, if it can be used, the binding's _bind.so."""
     global _lib, _bind
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
         raise ImportError(f"libjet.so not built at {path}: run linear_attention_lm_gen_b200/build.py")
-    _bind = importlib.import_module("._bind", __name__)
+    _bind = _load_bind()
     _lib = declare(ctypes.CDLL(path))
     return _lib
 
@@ -512,8 +529,8 @@ def jet_conv_gdn_decode_step(q, k, v, hist_in, hist_out, taps, g, beta, S, o=Non
 # ---------------------------------------------------------------- softmax attention over a paged cache
 # The decode step's calls take a few microseconds on the GPU. With outputs and
 # workspace given, on the current device and stream, they go through _bind,
-# which checks the arguments natively; anything else, and every error, through
-# the checks here.
+# which checks the arguments natively; anything else, every error, and every
+# call where _bind cannot be loaded, through the checks here.
 class _on:
     """Make device `index` current and issue on `stream` (default: the device's
     current stream) for the length of a call; what the call allocates belongs
@@ -637,7 +654,7 @@ def jet_attn_rope_append(q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, pag
     and page_table [nseq,max_pages] are int32 on the GPU. q_out may be q
     itself. Returns q_out [N,Hq,d]."""
     L = _lib or load_library()
-    if stream is None and q_out is not None:
+    if _bind is not None and stream is None and q_out is not None:
         st = _bind.rope_append(L.at_jet_attn_rope_append, q, k, v, q_gamma, k_gamma, inv_freq, cu_q, kv_lens, page_table,
                                k_pool, v_pool, q_out, eps, interleaved)
         if st == 0:
@@ -689,7 +706,7 @@ def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 
     max_new: the largest number of new tokens of a sequence (0: unknown); it
     only chooses the kernel. Returns o [N,Hq,d]."""
     L = _lib or load_library()
-    if stream is None and workspace is not None and o is not None:
+    if _bind is not None and stream is None and workspace is not None and o is not None:
         st = _bind.attn_paged(L.at_jet_attn_paged, q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new, o, workspace,
                               window, scale)
         if st == 0:
@@ -777,7 +794,7 @@ def jet_cache_copy(pools, src, dst, *, stream=None) -> None:
     each entry dense), entry dst[i] becomes a copy of entry src[i]. src and dst
     are host lists; a destination appears once and is no source."""
     L = _lib or load_library()
-    if stream is None:
+    if _bind is not None and stream is None:
         st = _bind.cache_copy(L.at_jet_cache_copy, pools, src, dst)
         if st == 0:
             return
@@ -805,7 +822,7 @@ def jet_cache_compact(pools, page_table, kv_lens, page_size: int, page_table_out
     (page_table_out, n_live [1]): the rewritten tables (page_table itself may
     be given) and the number of live pages, on the GPU."""
     L = _lib or load_library()
-    if stream is None and workspace is not None:
+    if _bind is not None and stream is None and workspace is not None:
         st = _bind.cache_compact(L.at_jet_cache_compact, pools, page_table, kv_lens, page_size, page_table_out, n_live,
                                  workspace)
         if st == 0:

@@ -50,24 +50,36 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return out
 
 
+def bind_abi() -> str:
+    """What _bind.so is built against: it calls torch's C++ interface and CPython's own."""
+    import torch
+    return f"torch {torch.__version__} {sys.implementation.cache_tag}"
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/bind.cpp, a CPython module on torch's C++ interface, into _bind.so."""
-    header = os.path.join(INCLUDE, "jet.h")
-    if not force and os.path.exists(BIND) and all(os.path.getmtime(s) <= os.path.getmtime(BIND)
-                                                  for s in (BIND_SRC, header)):
-        return BIND
+    """Compile csrc/bind.cpp, a CPython module on torch's C++ interface, into
+    _bind.so. _bind.abi beside it says for which torch and Python."""
+    header, stamp, abi = os.path.join(INCLUDE, "jet.h"), os.path.splitext(BIND)[0] + ".abi", bind_abi()
+    if not force and os.path.exists(BIND) and os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == abi
+        if same and all(os.path.getmtime(s) <= os.path.getmtime(BIND) for s in (BIND_SRC, header)):
+            return BIND
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], BIND_SRC, "-o",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DJET_BIND_ABI="{abi}"',
+           *[f"-I{d}" for d in inc], BIND_SRC, "-o",
            BIND + ".tmp", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(BIND + ".tmp", BIND)
+    with open(stamp, "w") as f:
+        f.write(abi)
     return BIND
 
 

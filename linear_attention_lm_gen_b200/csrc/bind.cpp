@@ -281,4 +281,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind(void) { return PyModule_Create(&kModule); }
+// `abi`: the torch and Python that it was compiled for, compared by the package before any call
+PyMODINIT_FUNC PyInit__bind(void) {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m && PyModule_AddStringConstant(m, "abi", JET_BIND_ABI) < 0) Py_CLEAR(m);
+    return m;
+}
