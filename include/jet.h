@@ -451,7 +451,8 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
  *   q_gamma, k_gamma [d] float32, or both NULL for no norm.
  *   inv_freq [rot/2] float32 (may be NULL for rot 0); rot a multiple of 8, at most d.
  *   q_out [N,Hq,d] with q_out_stride: the rotated queries; may be q itself
- *     (same stride), otherwise must not overlap an input.
+ *     (same stride, no element shared with k or v), otherwise must not overlap
+ *     an input.
  *   k and v of every new token go to its position in k_pool / v_pool.
  * A token without a position (kv_lens[s] below the number of new tokens)
  * leaves q_out and the cache untouched. Two new tokens never share a

@@ -52,6 +52,15 @@ size_t pool_extent(const AttnShape& a, int64_t page_stride, int64_t head_stride,
                                   (a.page_size - 1) * row_stride + a.d);
 }
 
+// N rows of wa elements every sa from a, and of wb every sb from b: an element in common? With one stride exactly, but
+// for rows of b before the first or behind the last of a; with two wherever one's extent meets the other's.
+bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int N, size_t es) {
+    if (!overlap(a, es * (size_t)((N - 1) * sa + wa), b, es * (size_t)((N - 1) * sb + wb))) return false;
+    if (sa != sb) return true;
+    const int64_t S = sa * (int64_t)es, diff = (int64_t)((uintptr_t)b - (uintptr_t)a), r = (diff % S + S) % S;
+    return r < wa * (int64_t)es || r + wb * (int64_t)es > S;
+}
+
 template <typename T, int LPR, int E, bool INTER>
 jet_status launch_append_t(const attn::AppendArgs& a, const attn::Cache& c, const attn::Batch& b, cudaStream_t s) {
     // four tokens to a block once that still fills the GPU several times over
@@ -228,17 +237,21 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
                           (const void*)kv_lens, (const void*)page_table})
         if (!aligned_to(p, 4)) return JET_ERR_MISALIGNED;
     auto span = [&](int64_t sd, int heads) { return es * (size_t)((int64_t)(N - 1) * sd + (int64_t)heads * d); };
-    // in place over q (same rows), or apart from every input; the pools apart from all of them
-    if (!(q_out == q && q_out_stride == q_stride))
+    // in place over q (same rows, apart from those of k and v), or apart from every input; the pools apart from all of them
+    if (q_out == q && q_out_stride == q_stride) {
+        for (auto [p, sd] : {std::pair<const void*, int64_t>{k, k_stride}, {v, v_stride}})
+            if (rows_overlap(q, q_stride, (int64_t)Hq * d, p, sd, (int64_t)Hk * d, N, es)) return JET_ERR_INVALID_ARG;
+    } else {
         for (auto [p, n] : {std::pair<const void*, size_t>{q, span(q_stride, Hq)}, {k, span(k_stride, Hk)},
                             {v, span(v_stride, Hk)}})
             if (overlap(q_out, span(q_out_stride, Hq), p, n)) return JET_ERR_INVALID_ARG;
+    }
     const size_t ext = pool_extent(a, page_stride, head_stride, row_stride);
     for (const void* pool : {(const void*)k_pool, (const void*)v_pool})
         for (auto [p, n] : {std::pair<const void*, size_t>{q, span(q_stride, Hq)}, {k, span(k_stride, Hk)},
                             {v, span(v_stride, Hk)}, {q_out, span(q_out_stride, Hq)}})
             if (overlap(pool, ext, p, n)) return JET_ERR_INVALID_ARG;
-    if (k_pool == v_pool) return JET_ERR_INVALID_ARG;
+    if (overlap(k_pool, es * d, v_pool, es * d)) return JET_ERR_INVALID_ARG;       // with the same strides: every row
     const attn::AppendArgs args{q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_gamma, k_gamma, inv_freq, q_out,
                                 Hq, Hk, d, rot, eps};
     const attn::Cache c{k_pool, v_pool, page_stride, head_stride, row_stride, page_table, max_pages, n_pages,
