@@ -476,6 +476,8 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
  *   j from max(0, p - window + 1) (0 when window is 0) to p, p the position of token i.
  *   q [N,Hq,d], q_stride elements between tokens; o [N,Hq,d] dense, must not
  *     overlap q or the pools. A token that sees no position (p < 0) gets zeros.
+ *   nseq * N * Hq * (max_pages * page_size + N + 1024) at most 2^62, else
+ *     JET_ERR_UNSUPPORTED.
  *   max_new: the largest number of new tokens of a sequence, or 0 if unknown.
  *     It only chooses the kernel; any value gives correct results.
  *   workspace: jet_attn_paged_workspace_size bytes (16-byte aligned; independent

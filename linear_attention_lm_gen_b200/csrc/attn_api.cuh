@@ -283,6 +283,9 @@ jet_status jet_attn_paged(const void* q, int64_t q_stride, const void* k_pool, c
     jet_status st = check_attn_shape(a);
     if (st != JET_OK) return st;
     if (window < 0 || max_new < 0 || !(scale > 0.f && scale < INFINITY)) return JET_ERR_INVALID_ARG;
+    // The axis of the work is measured in 64 bits. Offsets are device data, so every sequence may claim all rows; one
+    // costs at most its rows times heads times positions (or rows, if it claims more of them) and a constant below 1024.
+    if ((double)nseq * N * Hq * ((double)max_pages * page_size + N + 1024.0) > 0x1p62) return JET_ERR_UNSUPPORTED;
     if (q_stride < (int64_t)Hq * d || q_stride > kMaxTokenStride) return JET_ERR_INVALID_ARG;
     if (q_stride % 8 != 0) return JET_ERR_MISALIGNED;
     st = check_pools(a, k_pool, v_pool, page_stride, head_stride, row_stride);
