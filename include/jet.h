@@ -436,8 +436,14 @@ jet_status jet_jetblock_layer(const void* x, const void* wq, const void* wk, con
  * Shapes: Hq a multiple of Hk (head h of q reads head h / (Hq / Hk) of the
  *   cache), Hq <= 256, Hq / Hk <= 64; d a multiple of 16, at most 128;
  *   nseq <= 65535; max_pages * page_size at most 2^30, N at most 2^24.
- * q, k, v and the pools have the storage type dt (JET_BF16 or JET_F32); all
- * arithmetic is float32, results are rounded once.
+ * q, k, v and the pools have the storage type dt (JET_BF16 or JET_F32).
+ *   Arithmetic is float32 and results are rounded once, with one exception:
+ *   jet_attn_paged in bf16 rounds the softmax weights to bf16 before their
+ *   product with V (the sum they are divided by is of the unrounded ones),
+ *   which adds at most 2^-8 sum_j w_j |v_j| to an output's error, half a step
+ *   of each weight. Against 64 bits the error of normal inputs is 0.0014 to
+ *   0.0023 of the result, where the result's own rounding alone makes 0.0012
+ *   to 0.0017.
  * ---------------------------------------------------------------------- */
 
 /*
@@ -479,7 +485,11 @@ jet_status jet_attn_rope_append(const void* q, int64_t q_stride, const void* k, 
  *   nseq * N * Hq * (max_pages * page_size + N + 1024) at most 2^62, else
  *     JET_ERR_UNSUPPORTED.
  *   max_new: the largest number of new tokens of a sequence, or 0 if unknown.
- *     It only chooses the kernel; any value gives correct results.
+ *     It only chooses the kernel; any value gives correct results. 0 stands
+ *     for the average: give the number where a few prompt pieces go with many
+ *     single tokens, since the kernel for single tokens reads the cache again
+ *     for every 16 rows (255 tokens and a piece of 500 over 100000 positions:
+ *     0.3 to 0.9 ms with it, 1.9 to 6.9 ms without).
  *   workspace: jet_attn_paged_workspace_size bytes (16-byte aligned; independent
  *     of the cache's lengths), else JET_ERR_WORKSPACE before any launch.
  *     Contents on entry are ignored; calls that share one must be ordered.

@@ -703,8 +703,10 @@ def jet_attn_paged(q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new: int = 
     of their sequences (append theirs first): pools [pages,Hk,page,d], cu_q,
     kv_lens and page_table as in jet_attn_rope_append. window: positions a
     token sees, its own included (0: all). scale: 1/sqrt(d) by default.
-    max_new: the largest number of new tokens of a sequence (0: unknown); it
-    only chooses the kernel. Returns o [N,Hq,d]."""
+    max_new: the largest number of new tokens of a sequence; it only chooses
+    the kernel (0: by their average, slow for a long piece among many single
+    tokens). In bf16 the softmax weights are rounded to bf16 before their
+    product with V. Returns o [N,Hq,d]."""
     L = _lib or load_library()
     if _bind is not None and stream is None and workspace is not None and o is not None:
         st = _bind.attn_paged(L.at_jet_attn_paged, q, k_pool, v_pool, cu_q, kv_lens, page_table, max_new, o, workspace,

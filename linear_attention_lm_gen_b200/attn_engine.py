@@ -22,7 +22,11 @@ grows with the sequence; this module keeps it in pages:
 
 All layers share the page numbering: page i is entry i of every layer's pools.
 If every layer has a window, pages that lie before all windows are given up as
-the sequences advance. The host keeps the page tables and reference counts;
+the sequences advance. One layer that sees everything keeps every page, for
+the windowed layers too: a model that mixes the two (as the 2B and 4B ones do)
+saves their memory with two engines, one for the layers without a window and
+one for those with, each with its own pages, whose begin, fork and release are
+called alike. The host keeps the page tables and reference counts;
 each step sends its tables to the GPU in one copy. Everything is issued on
 torch's current stream. Steps on two streams share no scratch memory, but the
 pages: a step that gives pages up or takes them has to be ordered with the

@@ -196,6 +196,14 @@ jet_status launch_attn_chunk(const void* q, int64_t q_stride, const attn::Cache&
 // an item's ends (12 heads over 2; us, decode against chunk kernel: 128 tokens
 // over 500 19 / 23, 8 x 8 over 500 16 / 21, 8 x 32 over nothing 11 / 13;
 // 8 x 32 over 500 25 / 24, 64 over 3000 26 / 24, 8 x 128 over nothing 28 / 14).
+// The bound was fitted on that head shape; at d 64 (16 heads over 8) the decode
+// kernel stays ahead longer (4 tokens x 32 over 2000 34 / 57).
+//
+// Without max_new the average stands for it. That is right for the batches whose
+// sequences are alike (2 tokens x 32 over 2000, 12 heads over 2: 28 / 38; 128 x 2
+// over 4000, 32 over 8: 326 / 449) and for a piece of 500 tokens among 255 single
+// ones over 2000 (10 over 2: 129 / 140), wrong by up to 7 times where such a piece
+// has a long cache (over 100000, 10 over 2: 1930 / 257): the caller's to say.
 constexpr double kDecodeWork = 1.5e6;
 bool take_decode(int nseq, int N, int max_new, long long table_positions, int Hq, int G, int window) {
     const long long typical = max_new > 0 ? max_new : (N + nseq - 1) / nseq;

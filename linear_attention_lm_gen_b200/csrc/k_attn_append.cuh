@@ -14,8 +14,9 @@
 // accesses in bf16) where the rotated part is a multiple of 16, else 4. Gammas,
 // cosines and sines are multiplied once per token into two coefficients an
 // element, kept in shared memory: applied row by row they made instructions the
-// limit, and in registers the occupancy. 14463 tokens of 20 heads: 38 us, 3.9
-// TB/s, of which the rows alone take 27; 256 tokens: 3.7 us.
+// limit, and in registers the occupancy. 14463 tokens of 20 heads: 38 to 40
+// us, 3.9 TB/s, of which the rows alone take 27; in float32 59 us, 5.0 TB/s;
+// 256 tokens: 3.7 to 4.1 us.
 // The angle is formed and reduced to a fraction of a turn in float64: at
 // position 200000 a float32 product would be off by up to 0.008 rad, more than
 // a bf16 step.

@@ -9,7 +9,9 @@
 // The matrix products of a step and tile take about 1024 tensor cycles, its
 // 128 x 128 exponentials 1024 cycles of the SM's special-function unit, so
 // the two tiles alternate: while one is in its softmax the other's products
-// run, and both units are near their limits together.
+// run. Neither unit is full: a step takes 3650 cycles, 56 % of either, since a
+// tile's softmax (1930 cycles) and products follow one another through two
+// hand-overs.
 //
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, the row's 128
 //                   scores in registers, no exchange between threads. The
@@ -38,8 +40,11 @@
 // rows that do see that value get it added when the results are written.
 //
 // Work is divided as k_attn_sched.cuh says, one CTA to an SM. 4096 new tokens
-// over 28672 (12 heads over 2, d 128): 620 us, 1.25 PFLOP/s; a step takes 3650
-// cycles, the products alone 2050.
+// over 28672 (12 heads over 2, d 128): 620 to 640 us in bursts of about 20
+// calls (1.21 to 1.25 PFLOP/s), 716 to 736 us in a long run of calls (1.05 to
+// 1.08), where the power limit lowers the clock; the products alone take 2050
+// of a step's cycles. 4096 over nothing 79 us, 512 over 2048 33 us: there the
+// ends of items and the join weigh most.
 #pragma once
 #include <cuda.h>
 

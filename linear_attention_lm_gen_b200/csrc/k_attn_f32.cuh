@@ -7,8 +7,12 @@
 // rows x 4 or 8 columns of the result; a row's 16 threads are half a warp, so the
 // running maximum and sum need four shuffles. A product is 64 fused
 // multiply-adds for every 8 loads of 16 bytes, which broadcast within a warp:
-// bound by the multiply-adds (0.35 of their rate over 3 sequences of 100 to 333
-// new tokens, 39 us; as packed pairs 43 us). Work is divided as k_attn_sched.cuh says, four
+// bound by the multiply-adds, those of masked positions and empty rows
+// included. 3 sequences of 100 to 333 new tokens 40 us (as packed pairs 43 us)
+// where the visible positions alone are 7.3 us of multiply-adds; 512 new tokens
+// over 2048 (12 heads over 2, d 128) 281 us of 101. The tile is the same for a
+// decode token, whose few rows leave most of it empty: 64 x 4000 positions 289
+// us where the bytes are 80. Work is divided as k_attn_sched.cuh says, four
 // CTAs to an SM for d <= 64 and two above.
 //
 // Positions outside the item's range are zero-filled, never read. A masked

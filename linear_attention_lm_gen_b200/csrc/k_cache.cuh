@@ -3,8 +3,11 @@
 //
 // Both are bandwidth-bound: every moved byte is read once and written once.
 // A block moves pieces of 16 KB, each thread four 16-byte loads in flight
-// before the first store. 64 states of 1.2 MB (32 read, 64 written): 17 us, 6.7
-// TB/s; a compaction that moves 0.54 GB of 8192 pages: 177 us, 6.1 TB/s.
+// before the first store. 64 states of 1.2 MB (32 read, 64 written), other
+// states every time: 20 us, 5.8 TB/s (the same ones again 17 us, part of them
+// then in L2); a compaction that moves 0.54 GB of 8192 pages: 174 to 178 us,
+// 6.1 to 6.2 TB/s, the plan of one block before it included. That plan is
+// what a smaller one waits for: 4096 pages, half of them live, 28 us of 20.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
