@@ -69,9 +69,13 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 size_t esize(jet_dtype dt) { return dt == JET_BF16 ? 2 : 4; }
 
-jet_status launch_status() {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? JET_OK : JET_ERR_CUDA;
+// What a runtime call returned. An error is also taken off the thread's
+// record; a call is judged by its own results, never by that record, where an
+// earlier call's error may still stand.
+jet_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return JET_OK;
+    cudaGetLastError();
+    return JET_ERR_CUDA;
 }
 
 // Launch with programmatic stream serialization allowed (the kernels wait
@@ -91,16 +95,14 @@ jet_status launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cu
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    if (e != cudaSuccess) return JET_ERR_CUDA;
-    return launch_status();
+    return cuda_status(e);
 }
 
 // opt a kernel into more than 48 KB of dynamic shared memory
 template <typename K>
 jet_status smem_attr(K kernel, size_t bytes) {
     if (bytes <= 48 * 1024) return JET_OK;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
-               ? JET_OK : JET_ERR_CUDA;
+    return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
 }
 
 bool dtype_ok(jet_dtype dt) { return dt == JET_F32 || dt == JET_BF16; }
@@ -133,8 +135,7 @@ jet_status launch_genconv_t(const void* x, const void* w1, const void* w2, const
                                              (const T*)hin, (T*)vout, (T*)hout, cw, B, Tn, D, H, dv, hpc, slots,
                                              n_slots);
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    if (e != cudaSuccess) return JET_ERR_CUDA;
-    return launch_status();
+    return cuda_status(e);
 }
 
 // One new token per sequence, bf16: the decode kernel (one round trip to
@@ -166,8 +167,7 @@ jet_status launch_genconv_decode_t(const void* x, const void* w1, const void* w2
                                              (const __nv_bfloat16*)hin, (__nv_bfloat16*)vout, (__nv_bfloat16*)hout, cw,
                                              B, D, H, dv, hpc, per, slots, n_slots);
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    if (e != cudaSuccess) return JET_ERR_CUDA;
-    return launch_status();
+    return cuda_status(e);
 }
 
 jet_status launch_genconv_decode(const void* x, const void* w1, const void* w2, const void* v, const void* hin,
