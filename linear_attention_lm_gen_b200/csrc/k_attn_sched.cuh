@@ -133,8 +133,8 @@ __device__ __forceinline__ bool block_locate(const Work& w, int n_cta, int index
         if (i < warp) before += part[i];
         total += part[i];
     }
-    // n_cta chunks reach behind the end; the shift is 0 but where float64 rounds by more than the 1 makes up for
-    chunk = (long long)((double)total / n_cta) + 1 + (total >> 50);
+    // n_cta chunks reach behind the end: the factor outweighs float64's roundings where the 1 no longer does
+    chunk = (long long)((double)total / n_cta * (1.0 + 0x1p-50)) + 1;
     chunk = max((long long)w.min_chunk, chunk);
     const long long x = chunk * index;
     if (x >= total) return false;

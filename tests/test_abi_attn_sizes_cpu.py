@@ -43,5 +43,7 @@ def test_the_limit_covers_the_cost_of_every_batch():
     # the chunks of a grid of up to 592 reach the end, whatever the rounding in float64
     for total in [1, 100, 147, 148, 2 ** 40 + 1, 2 ** 50 - 1, 2 ** 50 + 77, 2 ** 53 + 1, 2 ** 57 - 1, 2 ** 61 + 12345, 2 ** 62]:
         for grid in (1, 132, 147, 148, 296, 444, 592):
-            chunk = int(float(total) / grid) + 1 + (total >> 50)
-            assert chunk * grid > total and (chunk - 1 - (total >> 50)) <= total / grid * (1 + 1e-15) + 1
+            chunk = int(float(total) / grid * (1.0 + 2.0 ** -50)) + 1
+            assert chunk * grid > total and chunk - 1 <= total / grid * (1 + 1e-15) + 1
+            if total <= 2 ** 40:
+                assert chunk == total // grid + 1

@@ -20,7 +20,7 @@ def jet():
 
 
 # in increasing order: a larger call before a smaller one would have asked for more
-@pytest.mark.parametrize("P", [262144, 262145, 392000, 392192, 392800, 393216, 393217, 600001, 1 << 20])
+@pytest.mark.parametrize("P", [262144, 262145, 385024, 385056, 392192, 392800, 393216, 393217, 600001, 1 << 20])
 def test_page_numbers_up_to_the_limit(jet, P):
     r = np.random.default_rng(P)
     page, seqs, width = 16, 40, 50
