@@ -40,11 +40,10 @@
 // rows that do see that value get it added when the results are written.
 //
 // Work is divided as k_attn_sched.cuh says, one CTA to an SM. 4096 new tokens
-// over 28672 (12 heads over 2, d 128): 620 to 640 us in bursts of about 20
-// calls (1.21 to 1.25 PFLOP/s), 716 to 736 us in a long run of calls (1.05 to
-// 1.08), where the power limit lowers the clock; the products alone take 2050
-// of a step's cycles. 4096 over nothing 79 us, 512 over 2048 33 us: there the
-// ends of items and the join weigh most.
+// over 28672 (12 heads over 2, d 128): 618 us in bursts of about 20 calls (1.25
+// PFLOP/s), 716 us in a long run of calls (1.08), where the power limit lowers
+// the clock; the products alone take 2050 of a step's cycles. 4096 over nothing
+// 77 us, 512 over 2048 33 us: there the ends of items and the join weigh most.
 #pragma once
 #include <cuda.h>
 

@@ -10,8 +10,8 @@
 // bound by the multiply-adds, those of masked positions and empty rows
 // included. 3 sequences of 100 to 333 new tokens 40 us (as packed pairs 43 us)
 // where the visible positions alone are 7.3 us of multiply-adds; 512 new tokens
-// over 2048 (12 heads over 2, d 128) 281 us of 101. The tile is the same for a
-// decode token, whose few rows leave most of it empty: 64 x 4000 positions 289
+// over 2048 (12 heads over 2, d 128) 279 us of 101. The tile is the same for a
+// decode token, whose few rows leave most of it empty: 64 x 4000 positions 288
 // us where the bytes are 80. Work is divided as k_attn_sched.cuh says, four
 // CTAs to an SM for d <= 64 and two above.
 //
